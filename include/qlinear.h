@@ -33,6 +33,15 @@
  *                     before both scales are applied.  M <= 16 runs
  *                     the weight-streaming decode kernel on E4M3 mma.sync,
  *                     M >= 17 the tensor-core E4M3 GEMM.
+ *   QL_MXFP4_G32      microscaled 4-bit floating point: E2M1 codes (0, 0.5, 1,
+ *                     1.5, 2, 3, 4, 6 and their negatives) under one
+ *                     power-of-two scale per row per 32 of K, as the Open
+ *                     Compute Project's Microscaling Formats specification
+ *                     defines MXFP4; x is bf16.  No card ships it: it is the
+ *                     4-bit format that this GPU's tensor cores multiply as it
+ *                     is stored.
+ *   QL_MXFP4A4_G32    the same packed weights with MXFP4 activations: x is
+ *                     quantised as act_quant_mxfp4 does.
  * Flag QL_HADAMARD: the weights live in the 128-wide Walsh-Hadamard domain
  * ("transform=fwht128" in the recipe of "gemma4-26b-a4b-dflash-i8"); the
  * forward pass rotates each 128-block of x by the same orthonormal transform
@@ -46,6 +55,13 @@
  *     stream with code k in stream bits 5k..5k+4.
  *   scales: [N][K/g] of bf16 or f16 (g = 128, or 64 for int4); fp8 block
  *     scales [ceil(N/128)][K/128] bf16.  zeros (int5 only): [N][K/128] u8.
+ *   MXFP4 codes: [N][K/2] bytes, code k of a row in byte k/2, low nibble for
+ *     even k; sign in the nibble's bit 3, then two exponent bits and one
+ *     mantissa bit.  MXFP4 scales: bytes e + 127 for the scale 2^e (255: the
+ *     block is NaN), in blocks of 128 rows x 128 of K,
+ *     [ceil(N/128)][K/128][32][4][4]: byte [r % 32][r % 128 / 32][k % 128 / 32]
+ *     of block [r / 128][k / 128] is the scale of row r at column k; bytes of
+ *     rows past N are 0.
  *
  * Conventions for every call:
  *   - All data pointers are DEVICE pointers owned by the caller, except the
@@ -91,7 +107,9 @@ typedef enum {
     QL_I4_G64_BF16 = 4,
     QL_I5Z_G128_F16 = 5,
     QL_FP8_B128_BF16 = 6,
-    QL_FP8A8_B128_BF16 = 7
+    QL_FP8A8_B128_BF16 = 7,
+    QL_MXFP4_G32 = 16,
+    QL_MXFP4A4_G32 = 17
 } ql_fmt;
 
 /* QL_SCALE_SEARCH: a rule for qlinear_pack's mode (a), int8 formats (1, 2, 3)
@@ -135,8 +153,11 @@ int qlinear_packed_sizes(int fmt, int N, int K, size_t* codes_bytes, size_t* sca
  *      the squared error sum_k (w_k - s_i q_k)^2 over k = 0..127 in order, each
  *      operation rounded to fp64; the least error wins, the smaller i on a
  *      tie (i = 0 is the plain round-to-nearest result).
+ *      MXFP4: as act_quant_mxfp4 on the fp32 (rotated) weight.
  *  (b) codes_in != NULL: pack given codes.  codes_in is int8 [N, K] (uint8 for
- *      int5, e4m3 bytes for fp8), scales_in the scales in the output layout,
+ *      int5, e4m3 bytes for fp8, code numbers 0..15 for MXFP4), scales_in the
+ *      scales in the output layout (MXFP4: row-major [N][K/32], as checkpoints
+ *      hold them; they are laid out in blocks),
  *      zeros_in the int5 zero points; they are copied / bit-packed.  A code
  *      outside its format's range is packed as 0 and flags QL_DEVERR_CODE_RANGE.
  *      QL_SCALE_SEARCH with given codes is QL_EINVAL.
@@ -154,7 +175,11 @@ int qlinear_workspace_size(int fmt, int flags, int M, int N, int K, size_t* byte
  *      int8 quantisation of (rotated) x, one fp32 scale per token per 128
  *      (as act_quant_i8_g128), and each 128-group's integer dot product is
  *      exact in int32 before its two scales are applied; the same for int5
- *      with M >= 65 (W5A8, codes q - z).
+ *      with M >= 65 (W5A8, codes q - z).  QL_MXFP4A4_G32: x~ is
+ *      act_quant_mxfp4 of (rotated) x.  QL_MXFP4_G32: x~ enters the tensor
+ *      cores as two E4M3 parts under one power-of-two scale per 32 values,
+ *      whose sum is exact for every value at least 2^-14 of the largest of its
+ *      32 and within 2^-22 of that largest otherwise.
  *   W_packed, scales, zeros: the packed weight (zeros only for int5).
  *   ws, ws_bytes: caller's device workspace, at least qlinear_workspace_size.
  * y is overwritten.  The floating-point sums may be accumulated in any order;
@@ -162,7 +187,10 @@ int qlinear_workspace_size(int fmt, int flags, int M, int N, int K, size_t* byte
  * Calls whose activations stay 16-bit (all formats but W8A8 and format 7, and
  * int5 up to 64 rows) stage one token row, in fp32 and f16, in shared memory:
  * they take K <= QL_A16_MAX_K and return QL_EUNSUPPORTED above it
- * (moe_gate_up likewise). */
+ * (moe_gate_up likewise).  The MXFP4 formats have no such limit here.
+ * MXFP4: W_packed is 32-byte aligned (QL_EALIGN otherwise); a row of x with
+ * a value that is not finite gives a row of y that is NaN, and a weight block
+ * with scale byte 255 a NaN column; the sums are bit-reproducible. */
 enum { QL_A16_MAX_K = 32768 };
 int qlinear_forward(const void* x, const void* W_packed, const void* scales, const uint8_t* zeros, int fmt,
                     int flags, int M, int N, int K, float* y, void* ws, size_t ws_bytes, void* stream);
@@ -200,6 +228,21 @@ int act_quant_i8_g128(const void* x, int M, int K, int rotate, int8_t* q, float*
  * s fp32 [M, K/128]. */
 int act_quant_e4m3_g128(const void* x, int M, int K, int rotate, uint8_t* q, float* s, void* stream);
 
+/* act_quant_mxfp4 -- per token per 32 values: on the fp32 block v (rotated as
+ * hadamard128_rotate but NOT rounded to bf16 when rotate != 0),
+ * e = max(floor(log2(max|v|)) - 2, -127), code = the E2M1 value nearest to
+ * v / 2^e, ties to the even code, at most 6 in magnitude; an all-zero block
+ * gets e = -127 and zeros; a block holding a value that is not finite gets
+ * scale byte 255 and zero codes.  x bf16 [M, K]; codes and scales in the packed
+ * MXFP4 layouts for M rows (sizes from qlinear_packed_sizes(QL_MXFP4_G32, M,
+ * K)). */
+int act_quant_mxfp4(const void* x, int M, int K, int rotate, uint8_t* codes, uint8_t* scales, void* stream);
+
+/* mxfp4_dequant -- the values that packed MXFP4 codes stand for: out bf16
+ * [N, K], each exact (a code times its scale has two significant bits; a product
+ * of 2^128 and above is infinite), NaN where the scale byte is 255. */
+int mxfp4_dequant(const uint8_t* codes, const uint8_t* scales, int N, int K, void* out, void* stream);
+
 /* hadamard128_rotate -- y = per-128-block orthonormal Walsh-Hadamard
  * transform of x along K, Sylvester order (the "attention join" of
  * "gemma4-26b-a4b-dflash-i8" writes the experts' input in this domain).
@@ -212,9 +255,10 @@ typedef struct {
     int E;              /* number of experts                                    */
     int N;              /* output rows per expert (gate and up halves together) */
     int K;              /* hidden size, multiple of 128                          */
-    int fmt;            /* QL_I8_G128_BF16, QL_I8_G128_F16, QL_FP8_B128_BF16 or
+    int fmt;            /* QL_I8_G128_BF16, QL_I8_G128_F16, QL_FP8_B128_BF16,
                            QL_FP8A8_B128_BF16 (the fp8 experts with E4M3
-                           activations, quantised once per token)            */
+                           activations, quantised once per token),
+                           QL_MXFP4_G32 or QL_MXFP4A4_G32                    */
     int flags;          /* QL_HADAMARD when the experts are in the rotated domain */
     const void* codes;  /* device, [E] consecutive packed weights of [N, K]      */
     const void* scales; /* device, [E] consecutive scale arrays                  */
@@ -243,9 +287,25 @@ int moe_workspace_size(const ql_experts* experts, int T, int topk, size_t* bytes
  * topk_weights (fp32 [T, topk], may be NULL) is accepted but not applied:
  * the routing weight belongs after the down projection.  Internally:
  * rotate, permute, grouped expert GEMM, and un-permute fused into the GEMM's
- * output stores.  `experts` is a host pointer. */
+ * output stores.  With the MXFP4 formats x~ and the product are
+ * qlinear_forward's (codes 32-byte aligned); rows of pairs with an id outside
+ * [0, E) are zero.  `experts` is a host pointer. */
 int moe_gate_up(const void* x, const int32_t* topk_ids, const float* topk_weights, const ql_experts* experts,
                 int T, int topk, float* y, void* ws, size_t ws_bytes, void* stream);
+
+/* Workspace bytes qlinear_grouped needs for R rows. */
+int qlinear_grouped_workspace_size(const ql_experts* experts, int R, size_t* bytes);
+
+/* qlinear_grouped -- qlinear_forward over rows that are already sorted by
+ * expert, with ragged counts, MXFP4 formats (others QL_EUNSUPPORTED):
+ *   y[r, :] = x~[r, :] . dequant(W_e)^T   for offsets[e] <= r < offsets[e + 1].
+ * x bf16 [R, K]; offsets int32 [E + 1] (device), non-decreasing, in [0, R], as
+ * moe_permute makes them; y fp32 [R, N].  Rows outside every segment (before
+ * offsets[0], from offsets[E] on) are neither read nor written.  An expert whose
+ * two offsets are out of order or out of [0, R] is skipped and sets
+ * QL_DEVERR_BOUNDS.  E <= 1024; `experts` is a host pointer; codes 32-byte aligned. */
+int qlinear_grouped(const void* x, const int32_t* offsets, const ql_experts* experts, int R, float* y, void* ws,
+                    size_t ws_bytes, void* stream);
 
 /* Stacked bf16 down-projection weights of the routed experts. */
 typedef struct {
@@ -323,7 +383,9 @@ enum {
     QL_KIND_PREFILL = 8,     /* tensor-core prefill GEMM                        */
     QL_KIND_PREFILL_PREP = 9, /* weight scales transposed for the prefill GEMM  */
     QL_KIND_MOE_ACT = 10,     /* gelu(gate) * up ahead of the down projection   */
-    QL_KIND_MOE_DOWN = 11     /* experts' down projection with the combine       */
+    QL_KIND_MOE_DOWN = 11,    /* experts' down projection with the combine       */
+    QL_KIND_MX_GEMM = 12,     /* MXFP4 product (grouped: QL_KIND_MOE_GEMM)       */
+    QL_KIND_MX_DEQUANT = 13   /* values of packed MXFP4 codes                    */
 };
 int ql_trace_enable(int capacity);
 int ql_trace_read(int* kinds, float* ms, int max, int* count);

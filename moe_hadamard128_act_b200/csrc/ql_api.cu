@@ -16,7 +16,8 @@ __device__ __align__(16) unsigned g_ql_state[4];
 void packed_sizes(int fmt, size_t N, size_t K, size_t* codes, size_t* scales, size_t* zeros) {
     *codes = N * fmt_row_bytes(fmt, K);
     *zeros = fmt == QL_I5Z_G128_F16 ? N * (K / 128) : 0;
-    if (fmt_fp8_weights(fmt)) *scales = ((N + 127) / 128) * (K / 128) * 2;
+    if (fmt_mxfp4(fmt)) *scales = ((N + 127) / 128) * (K / 128) * 512;
+    else if (fmt_fp8_weights(fmt)) *scales = ((N + 127) / 128) * (K / 128) * 2;
     else *scales = N * (K / fmt_group(fmt)) * 2;
 }
 
@@ -105,6 +106,10 @@ using namespace ql;
 namespace {
 
 bool aligned16(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 15u) == 0; }
+// MXFP4 codes: the TMA copies that spread 4-bit values over bytes want a 32-byte aligned matrix.
+bool aligned_codes(int fmt, const void* p) {
+    return (reinterpret_cast<uintptr_t>(p) & (fmt_mxfp4(fmt) ? 31u : 15u)) == 0;
+}
 thread_local cudaError_t g_last_cuda = cudaSuccess;  // reported by ql_last_cuda_error
 int from_cuda(cudaError_t e) {
     if (e == cudaSuccess) return QL_OK;
@@ -154,6 +159,49 @@ FwdWs forward_ws(int fmt, size_t M, size_t N, size_t K) {
         if (fmt == QL_I4_G64_BF16) w.g_bytes = align_up(M * (K / 64) * 4, 256);
     }
     return w;
+}
+
+// The MXFP4 product over R rows: quantised activations, their scales in the order of the product's tiles,
+// and, for pairs given by routing ids, their permutation.
+struct MxWs {
+    int nt, nblk;
+    size_t xq, xs, counts, offsets, perm, total;
+};
+MxWs mx_ws(int fmt, long long R, long long K, int E, bool pairs) {
+    const bool a16 = fmt == QL_MXFP4_G32;
+    MxWs w;
+    w.nt = mx_tokens(a16, (int)R, E);
+    w.nblk = mx_nblk(a16, w.nt);
+    size_t o = 0;
+    w.xq = o; o += align_up((size_t)R * (a16 ? 2 * K : K / 2), 256);
+    w.xs = o; o += align_up((size_t)mx_slots((int)R, E, w.nt) * (K / 128) * w.nblk * 512, 256);
+    w.counts = w.offsets = w.perm = 0;
+    if (pairs) {
+        w.counts = o; o += align_up((size_t)E * 4, 256);
+        w.offsets = o; o += align_up(((size_t)E + 1) * 4, 256);
+        w.perm = o; o += align_up((size_t)R * 4, 256);
+    }
+    w.total = o;
+    return w;
+}
+
+// Quantise the activations, then the product.  E = 0: one weight over every row.
+int mx_product(const void* x, const void* codes, const void* scales, int fmt, int flags, int R, int N, int K, int E,
+               const int32_t* offsets, const int32_t* perm, int topk, const MxWs& w, uint8_t* ws, float* y,
+               unsigned* err, cudaStream_t s) {
+    const bool a16 = fmt == QL_MXFP4_G32;
+    MxAct q{static_cast<const __nv_bfloat16*>(x), R, K, (flags & QL_HADAMARD) ? 1 : 0, w.nt, w.nblk, offsets, E, perm,
+            topk, ws + w.xq, ws + w.xs};
+    int t = trace_begin(QL_KIND_ACT_QUANT, s);
+    cudaError_t e = launch_mx_act(q, a16, s);
+    trace_end(t, s);
+    if (e != cudaSuccess) return from_cuda(e);
+    MxGemm g{static_cast<const uint8_t*>(codes), static_cast<const uint8_t*>(scales), q.codes, q.scales, offsets, perm,
+             y, err, R, E ? E : 1, N, K, w.nt, w.nblk};
+    t = trace_begin(E ? QL_KIND_MOE_GEMM : QL_KIND_MX_GEMM, s);
+    e = launch_mx_gemm(g, a16, s);
+    trace_end(t, s);
+    return from_cuda(e);
 }
 
 int x_order(int fmt) {
@@ -216,11 +264,11 @@ int check_experts(const ql_experts* ex) {
     if (ex->flags & ~(QL_HADAMARD | QL_SCALE_SEARCH)) return QL_EINVAL;
     if (!fmt_valid(ex->fmt)) return QL_EINVAL;
     if (ex->fmt != QL_I8_G128_BF16 && ex->fmt != QL_I8_G128_F16 && ex->fmt != QL_FP8_B128_BF16 &&
-        ex->fmt != QL_FP8A8_B128_BF16)
+        ex->fmt != QL_FP8A8_B128_BF16 && !fmt_mxfp4(ex->fmt))
         return QL_EUNSUPPORTED;
     if (ex->K > QL_A16_MAX_K) return QL_EUNSUPPORTED;
     if (!ex->codes || !ex->scales) return QL_EINVAL;
-    if (!aligned16(ex->codes) || !aligned16(ex->scales)) return QL_EALIGN;
+    if (!aligned_codes(ex->fmt, ex->codes) || !aligned16(ex->scales)) return QL_EALIGN;
     return QL_OK;
 }
 
@@ -309,7 +357,10 @@ int qlinear_pack(const float* W, const void* codes_in, const void* scales_in, co
         if (!aligned16(W)) return QL_EALIGN;
         if (fmt == QL_I5Z_G128_F16) return QL_EUNSUPPORTED;
         const int t = trace_begin(QL_KIND_PACK, s);
-        const cudaError_t e = launch_pack_rtn(W, fmt, flags, N, K, codes_out, scales_out, s);
+        const cudaError_t e =
+            fmt_mxfp4(fmt) ? launch_mx_quant_weight(W, N, K, flags & QL_HADAMARD, static_cast<uint8_t*>(codes_out),
+                                                    static_cast<uint8_t*>(scales_out), s)
+                           : launch_pack_rtn(W, fmt, flags, N, K, codes_out, scales_out, s);
         trace_end(t, s);
         return from_cuda(e);
     }
@@ -322,6 +373,13 @@ int qlinear_pack(const float* W, const void* codes_in, const void* scales_in, co
     DeviceInfo di;
     cudaError_t e = device_info(&di);
     if (e != cudaSuccess) return from_cuda(e);
+    if (fmt_mxfp4(fmt)) {
+        const int t = trace_begin(QL_KIND_PACK, s);
+        e = launch_mx_pack(static_cast<const uint8_t*>(codes_in), static_cast<const uint8_t*>(scales_in), N, K,
+                           static_cast<uint8_t*>(codes_out), static_cast<uint8_t*>(scales_out), di.err_word, s);
+        trace_end(t, s);
+        return from_cuda(e);
+    }
     int t = trace_begin(QL_KIND_PACK, s);
     e = launch_pack_codes(codes_in, fmt, N, K, codes_out, di.err_word, s);
     trace_end(t, s);
@@ -341,7 +399,7 @@ int qlinear_workspace_size(int fmt, int flags, int M, int N, int K, size_t* byte
     if (!fmt_valid(fmt) || M < 1 || N < 1 || K < 128 || K % 128 || (flags & ~(QL_HADAMARD | QL_SCALE_SEARCH)) ||
         !bytes)
         return QL_EINVAL;
-    *bytes = forward_ws(fmt, M, N, K).total();
+    *bytes = fmt_mxfp4(fmt) ? mx_ws(fmt, M, K, 0, false).total : forward_ws(fmt, M, N, K).total();
     return QL_OK;
 }
 
@@ -352,10 +410,20 @@ int qlinear_forward(const void* x, const void* W_packed, const void* scales, con
     if (!x || !W_packed || !scales || !y) return QL_EINVAL;
     if (fmt == QL_I5Z_G128_F16 && !zeros) return QL_EINVAL;
     const bool a8 = fmt == QL_I8A8_G128_BF16 || fmt == QL_FP8A8_B128_BF16 || (fmt == QL_I5Z_G128_F16 && M >= kW5A8MinM);
-    if (!a8 && K > QL_A16_MAX_K) return QL_EUNSUPPORTED;
-    if (!aligned16(x) || !aligned16(W_packed) || !aligned16(scales) || !aligned16(y) ||
+    if (!a8 && !fmt_mxfp4(fmt) && K > QL_A16_MAX_K) return QL_EUNSUPPORTED;
+    if (!aligned16(x) || !aligned_codes(fmt, W_packed) || !aligned16(scales) || !aligned16(y) ||
         (zeros && !aligned16(zeros)))
         return QL_EALIGN;
+    if (fmt_mxfp4(fmt)) {
+        const MxWs w = mx_ws(fmt, M, K, 0, false);
+        if (!ws || ws_bytes < w.total) return QL_EWORKSPACE;
+        if (!aligned16(ws)) return QL_EALIGN;
+        DeviceInfo di;
+        const cudaError_t e = device_info(&di);
+        if (e != cudaSuccess) return from_cuda(e);
+        return mx_product(x, W_packed, scales, fmt, flags, M, N, K, 0, nullptr, nullptr, 1, w,
+                          static_cast<uint8_t*>(ws), y, di.err_word, static_cast<cudaStream_t>(stream));
+    }
     const FwdWs w = forward_ws(fmt, M, N, K);
     if (!ws || ws_bytes < w.total()) return QL_EWORKSPACE;
     if (!aligned16(ws)) return QL_EALIGN;
@@ -579,6 +647,26 @@ int act_quant_e4m3_g128(const void* x, int M, int K, int rotate, uint8_t* q, flo
     return from_cuda(e);
 }
 
+int act_quant_mxfp4(const void* x, int M, int K, int rotate, uint8_t* codes, uint8_t* scales, void* stream) {
+    if (M < 1 || K < 128 || K % 128 || !x || !codes || !scales) return QL_EINVAL;
+    if (!aligned16(x) || !aligned16(codes) || !aligned16(scales)) return QL_EALIGN;
+    cudaStream_t st = static_cast<cudaStream_t>(stream);
+    const int t = trace_begin(QL_KIND_ACT_QUANT, st);
+    const cudaError_t e = launch_mx_quant_rows(x, M, K, rotate ? 1 : 0, codes, scales, st);
+    trace_end(t, st);
+    return from_cuda(e);
+}
+
+int mxfp4_dequant(const uint8_t* codes, const uint8_t* scales, int N, int K, void* out, void* stream) {
+    if (N < 1 || K < 128 || K % 128 || !codes || !scales || !out) return QL_EINVAL;
+    if (!aligned16(codes) || !aligned16(scales) || !aligned16(out)) return QL_EALIGN;
+    cudaStream_t st = static_cast<cudaStream_t>(stream);
+    const int t = trace_begin(QL_KIND_MX_DEQUANT, st);
+    const cudaError_t e = launch_mx_dequant(codes, scales, N, K, out, st);
+    trace_end(t, st);
+    return from_cuda(e);
+}
+
 int hadamard128_rotate(const void* x, int M, int K, void* y, void* stream) {
     if (M < 1 || K < 128 || K % 128 || !x || !y) return QL_EINVAL;
     if (!aligned16(x) || !aligned16(y)) return QL_EALIGN;
@@ -608,7 +696,9 @@ int moe_workspace_size(const ql_experts* experts, int T, int topk, size_t* bytes
     int st = check_experts(experts);
     if (st != QL_OK) return st;
     if (T < 1 || topk < 1 || topk > 64 || !bytes) return QL_EINVAL;
-    *bytes = moe_ws(experts, T, topk).total;
+    if (fmt_mxfp4(experts->fmt) && (long long)T * topk > INT32_MAX) return QL_EINVAL;
+    *bytes = fmt_mxfp4(experts->fmt) ? mx_ws(experts->fmt, (long long)T * topk, experts->K, experts->E, true).total
+                                     : moe_ws(experts, T, topk).total;
     return QL_OK;
 }
 
@@ -619,6 +709,30 @@ int moe_gate_up(const void* x, const int32_t* topk_ids, const float* topk_weight
     if (st != QL_OK) return st;
     if (T < 1 || topk < 1 || topk > 64 || !x || !topk_ids || !y) return QL_EINVAL;
     if (!aligned16(x) || !aligned16(topk_ids) || !aligned16(y)) return QL_EALIGN;
+    if (fmt_mxfp4(experts->fmt)) {
+        if ((long long)T * topk > INT32_MAX) return QL_EINVAL;
+        const int R = T * topk;
+        const MxWs w = mx_ws(experts->fmt, R, experts->K, experts->E, true);
+        if (!ws || ws_bytes < w.total) return QL_EWORKSPACE;
+        if (!aligned16(ws)) return QL_EALIGN;
+        DeviceInfo di;
+        cudaError_t e = device_info(&di);
+        if (e != cudaSuccess) return from_cuda(e);
+        cudaStream_t s = static_cast<cudaStream_t>(stream);
+        uint8_t* const b = static_cast<uint8_t*>(ws);
+        int32_t* const counts = reinterpret_cast<int32_t*>(b + w.counts);
+        int32_t* const offsets = reinterpret_cast<int32_t*>(b + w.offsets);
+        int32_t* const perm = reinterpret_cast<int32_t*>(b + w.perm);
+        MoePermuteOut po;
+        po.yz = y;  // rows of pairs with a bad expert id are zeroed
+        po.N = experts->N;
+        const int t = trace_begin(QL_KIND_MOE_PERMUTE, s);
+        e = launch_moe_permute(topk_ids, T, topk, experts->E, counts, offsets, perm, po, di.err_word, s);
+        trace_end(t, s);
+        if (e != cudaSuccess) return from_cuda(e);
+        return mx_product(x, experts->codes, experts->scales, experts->fmt, experts->flags, R, experts->N, experts->K,
+                          experts->E, offsets, perm, topk, w, b, y, di.err_word, s);
+    }
     const MoeWs w = moe_ws(experts, T, topk);
     if (!ws || ws_bytes < w.total) return QL_EWORKSPACE;
     if (!aligned16(ws)) return QL_EALIGN;
@@ -714,6 +828,33 @@ int moe_gate_up(const void* x, const int32_t* topk_ids, const float* topk_weight
     e = launch_moe_skinny(a, s);
     trace_end(t, s);
     return from_cuda(e);
+}
+
+int qlinear_grouped_workspace_size(const ql_experts* experts, int R, size_t* bytes) {
+    const int st = check_experts(experts);
+    if (st != QL_OK) return st;
+    if (!fmt_mxfp4(experts->fmt)) return QL_EUNSUPPORTED;
+    if (R < 1 || !bytes) return QL_EINVAL;
+    *bytes = mx_ws(experts->fmt, R, experts->K, experts->E, false).total;
+    return QL_OK;
+}
+
+int qlinear_grouped(const void* x, const int32_t* offsets, const ql_experts* experts, int R, float* y, void* ws,
+                    size_t ws_bytes, void* stream) {
+    const int st = check_experts(experts);
+    if (st != QL_OK) return st;
+    if (!fmt_mxfp4(experts->fmt)) return QL_EUNSUPPORTED;
+    if (R < 1 || !x || !offsets || !y) return QL_EINVAL;
+    if (!aligned16(x) || !aligned16(offsets) || !aligned16(y)) return QL_EALIGN;
+    const MxWs w = mx_ws(experts->fmt, R, experts->K, experts->E, false);
+    if (!ws || ws_bytes < w.total) return QL_EWORKSPACE;
+    if (!aligned16(ws)) return QL_EALIGN;
+    DeviceInfo di;
+    const cudaError_t e = device_info(&di);
+    if (e != cudaSuccess) return from_cuda(e);
+    return mx_product(x, experts->codes, experts->scales, experts->fmt, experts->flags, R, experts->N, experts->K,
+                      experts->E, offsets, nullptr, 1, w, static_cast<uint8_t*>(ws), y, di.err_word,
+                      static_cast<cudaStream_t>(stream));
 }
 
 int moe_down_workspace_size(const ql_down_experts* experts, int T, int topk, size_t* bytes) {

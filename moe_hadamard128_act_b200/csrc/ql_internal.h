@@ -14,7 +14,9 @@
 namespace ql {
 
 // ---- format arithmetic -------------------------------------------------------
-inline bool fmt_valid(int f) { return f >= QL_I8_G128_BF16 && f <= QL_FP8A8_B128_BF16; }
+// Microscaled 4-bit floating point weights (both formats pack alike).
+inline bool fmt_mxfp4(int f) { return f == QL_MXFP4_G32 || f == QL_MXFP4A4_G32; }
+inline bool fmt_valid(int f) { return (f >= QL_I8_G128_BF16 && f <= QL_FP8A8_B128_BF16) || fmt_mxfp4(f); }
 // FP8 E4M3 weights with 128 x 128 block scales (formats 6 and 7 pack alike).
 inline bool fmt_fp8_weights(int f) { return f == QL_FP8_B128_BF16 || f == QL_FP8A8_B128_BF16; }
 inline bool fmt_scale_f16(int f) { return f == QL_I8_G128_F16 || f == QL_I5Z_G128_F16; }
@@ -24,6 +26,8 @@ inline int fmt_group(int f) { return f == QL_I4_G64_BF16 ? 64 : 128; }
 // Bytes of one packed row of K codes.
 inline size_t fmt_row_bytes(int f, size_t K) {
     switch (f) {
+    case QL_MXFP4_G32:
+    case QL_MXFP4A4_G32:
     case QL_I4_G64_BF16: return K / 2;
     case QL_I5Z_G128_F16: return K * 5 / 8;
     default: return K;
@@ -224,6 +228,46 @@ cudaError_t launch_moe_down(const MoeArgs& a, cudaStream_t s);
 // order); pairs with an id outside [0, E) are skipped.  Also zeroes out[0 .. nz).
 cudaError_t launch_moe_act(const float* h, const int32_t* ids, int P, int E, int I, __nv_bfloat16* act, float* out,
                            long long nz, cudaStream_t s, const int32_t* inv = nullptr);
+
+// ---- MXFP4 (k_mxfp4.cu, k_mxfp4_gemm.cu; layouts in mx_layout.cuh) -------------------------------
+cudaError_t launch_mx_quant_weight(const float* W, int N, int K, int rotate, uint8_t* codes, uint8_t* scales,
+                                   cudaStream_t s);
+cudaError_t launch_mx_quant_rows(const void* x, int M, int K, int rotate, uint8_t* codes, uint8_t* scales,
+                                 cudaStream_t s);
+cudaError_t launch_mx_pack(const uint8_t* codes_in, const uint8_t* scales_in, int N, int K, uint8_t* codes,
+                           uint8_t* scales, unsigned* err, cudaStream_t s);
+cudaError_t launch_mx_dequant(const uint8_t* codes, const uint8_t* scales, int N, int K, void* out, cudaStream_t s);
+// The product's activations: R rows, sorted by expert when offsets [E + 1] is given, from x row r or
+// perm[r] / topk; token blocks of at most nt rows, nblk scale blocks per 128 columns of a slot.
+struct MxAct {
+    const __nv_bfloat16* x;
+    int R, K, rotate;
+    int nt, nblk;
+    const int32_t* offsets;
+    int E;
+    const int32_t* perm;
+    int topk;
+    uint8_t* codes;   // E2M1 [R][K / 2], or E4M3 parts [2][R][K]
+    uint8_t* scales;  // [slots][K / 128][nblk][512]
+};
+cudaError_t launch_mx_act(const MxAct& a, bool a16, cudaStream_t s);
+constexpr int kMxTokens = 64;  // rows of a token block at most
+// Rows of a token block for this call, and the scale blocks and slots that follow from it.
+int mx_tokens(bool a16, int R, int E);
+inline int mx_nblk(bool a16, int nt) { return ((a16 ? 2 : 1) * nt + 127) / 128; }
+inline long long mx_slots(int R, int E, int nt) { return E ? (long long)R / nt + E + 1 : ((long long)R + nt - 1) / nt; }
+struct MxGemm {
+    const uint8_t* codes;   // [E][N][K / 2]
+    const uint8_t* scales;  // [E][ceil(N / 128)][K / 128][512]
+    const uint8_t* xq;      // MxAct's codes and scales
+    const uint8_t* xs;
+    const int32_t* offsets;  // null: one expert owns every row
+    const int32_t* perm;     // row r goes to y row perm[r]; null: to row r
+    float* y;                // [R][N]
+    unsigned* err;
+    int R, E, N, K, nt, nblk;
+};
+cudaError_t launch_mx_gemm(const MxGemm& a, bool a16, cudaStream_t s);
 
 // ---- launch trace (ql_trace_enable / ql_trace_read) --------------------------------------
 // trace_begin records a start event for one library launch when tracing is on

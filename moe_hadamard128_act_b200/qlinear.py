@@ -25,9 +25,12 @@ I4_G64_BF16 = 4
 I5Z_G128_F16 = 5
 FP8_B128_BF16 = 6
 FP8A8_B128_BF16 = 7  # the fp8 weights with E4M3 activations
+MXFP4_G32 = 16  # microscaled 4-bit floating point weights, bf16 activations
+MXFP4A4_G32 = 17  # the same weights with MXFP4 activations
 HADAMARD = 1
 SCALE_SEARCH = 2  # qlinear_pack of an fp32 W, int8 formats: the best of 21 scales per group
-FORMATS = (I8_G128_BF16, I8_G128_F16, I8A8_G128_BF16, I4_G64_BF16, I5Z_G128_F16, FP8_B128_BF16, FP8A8_B128_BF16)
+FORMATS = (I8_G128_BF16, I8_G128_F16, I8A8_G128_BF16, I4_G64_BF16, I5Z_G128_F16, FP8_B128_BF16, FP8A8_B128_BF16,
+           MXFP4_G32, MXFP4A4_G32)
 
 DEVERR_EXPERT_ID = 1
 DEVERR_CODE_RANGE = 2
@@ -74,6 +77,10 @@ _SIGS = {
     "qlinear_gemm_a8": (_I, [_P, _P, _P, _P, _I, _I, _I, _I, _P, _I, _P]),
     "act_quant_i8_g128": (_I, [_P, _I, _I, _I, _P, _P, _P]),
     "act_quant_e4m3_g128": (_I, [_P, _I, _I, _I, _P, _P, _P]),
+    "act_quant_mxfp4": (_I, [_P, _I, _I, _I, _P, _P, _P]),
+    "mxfp4_dequant": (_I, [_P, _P, _I, _I, _P, _P]),
+    "qlinear_grouped_workspace_size": (_I, [ctypes.POINTER(ql_experts), _I, _PSZ]),
+    "qlinear_grouped": (_I, [_P, _P, ctypes.POINTER(ql_experts), _I, _P, _P, _SZ, _P]),
     "hadamard128_rotate": (_I, [_P, _I, _I, _P, _P]),
     "moe_permute": (_I, [_P, _I, _I, _I, _P, _P, _P, _P]),
     "moe_workspace_size": (_I, [ctypes.POINTER(ql_experts), _I, _I, _PSZ]),
@@ -89,7 +96,7 @@ _SIGS = {
 }
 
 KIND_NAMES = {1: "rotate", 2: "act_quant", 3: "prep_a16", 4: "skinny", 5: "moe_permute", 6: "moe_gemm", 7: "pack",
-              8: "prefill", 9: "prefill_prep", 10: "moe_act", 11: "moe_down"}
+              8: "prefill", 9: "prefill_prep", 10: "moe_act", 11: "moe_down", 12: "mx_gemm", 13: "mx_dequant"}
 
 _lib = None
 
@@ -152,7 +159,7 @@ def _experts_struct(E, N, K, fmt, flags, codes, scales):
 
 
 def moe_workspace_size(E: int, N: int, K: int, fmt: int, flags: int, T: int, topk: int) -> int:
-    ex = ql_experts(E, N, K, fmt, flags, 16, 16)  # placeholder aligned pointers: only sizes are read
+    ex = ql_experts(E, N, K, fmt, flags, 32, 32)  # placeholder aligned pointers: only sizes are read
     b = ctypes.c_size_t()
     _check("moe_workspace_size", lib().moe_workspace_size(ctypes.byref(ex), T, topk, ctypes.byref(b)))
     return b.value
@@ -265,6 +272,38 @@ def act_quant_e4m3_g128(x: torch.Tensor, rotate: bool = False, stream=None):
     return q, s
 
 
+def _rows(x: torch.Tensor, fn: str):
+    if x.dtype != torch.bfloat16 or x.dim() != 2:
+        raise ValueError(f"{fn}: x must be a 2-D bf16 tensor")
+    return x.shape
+
+
+def act_quant_mxfp4(x: torch.Tensor, rotate: bool = False, stream=None):
+    """MXFP4 codes and scales (uint8, packed layouts for M rows) of bf16 x [M, K]."""
+    M, K = _rows(x, "act_quant_mxfp4")
+    cb, sb, _ = qlinear_packed_sizes(MXFP4_G32, M, K)
+    codes, scales = _empty(cb, x.device), _empty(sb, x.device)
+    with torch.cuda.device(x.device):
+        _check("act_quant_mxfp4", lib().act_quant_mxfp4(_ptr(x), M, K, int(rotate), _ptr(codes), _ptr(scales),
+                                                        _stream(stream)))
+    return codes[:cb], scales[:sb]
+
+
+def mxfp4_dequant(codes: torch.Tensor, scales: torch.Tensor, N: int, K: int, out: torch.Tensor | None = None,
+                  stream=None) -> torch.Tensor:
+    """The bf16 values [N, K] that packed MXFP4 codes and scales stand for."""
+    cb, sb, _ = qlinear_packed_sizes(MXFP4_G32, N, K)
+    if codes.numel() * codes.element_size() != cb or scales.numel() * scales.element_size() != sb:
+        raise ValueError(f"mxfp4_dequant: [{N}, {K}] takes {cb} code and {sb} scale bytes")
+    if out is None:
+        out = torch.empty((N, K), dtype=torch.bfloat16, device=codes.device)
+    elif out.dtype != torch.bfloat16 or tuple(out.shape) != (N, K):
+        raise ValueError(f"out must be a bf16 tensor of shape ({N}, {K})")
+    with torch.cuda.device(codes.device):
+        _check("mxfp4_dequant", lib().mxfp4_dequant(_ptr(codes), _ptr(scales), N, K, _ptr(out), _stream(stream)))
+    return out
+
+
 def hadamard128_rotate(x: torch.Tensor, out: torch.Tensor | None = None, stream=None) -> torch.Tensor:
     M, K = x.shape
     y = torch.empty_like(x) if out is None else out
@@ -300,6 +339,40 @@ def moe_gate_up(x: torch.Tensor, topk_ids: torch.Tensor, codes: torch.Tensor, sc
     st = lib().moe_gate_up(_ptr(x), _ptr(topk_ids), _ptr(topk_weights), ctypes.byref(ex), T, topk, _ptr(y),
                            _ptr(ws), ws.numel(), _stream(stream))
     _check("moe_gate_up", st)
+    return y
+
+
+def qlinear_grouped_workspace_size(E: int, N: int, K: int, fmt: int, flags: int, R: int) -> int:
+    ex = ql_experts(E, N, K, fmt, flags, 32, 32)  # placeholder aligned pointers: only sizes are read
+    b = ctypes.c_size_t()
+    _check("qlinear_grouped_workspace_size",
+           lib().qlinear_grouped_workspace_size(ctypes.byref(ex), R, ctypes.byref(b)))
+    return b.value
+
+
+def qlinear_grouped(x: torch.Tensor, offsets: torch.Tensor, codes: torch.Tensor, scales: torch.Tensor, E: int, N: int,
+                    fmt: int = MXFP4A4_G32, flags: int = 0, y: torch.Tensor | None = None,
+                    ws: torch.Tensor | None = None, stream=None) -> torch.Tensor:
+    """y [R, N] fp32: row r of bf16 x [R, K] times its expert's packed MXFP4 weight, expert e owning the rows
+    offsets[e] .. offsets[e + 1] (int32 [E + 1] on the device).  Rows outside every segment are left as they
+    were: uninitialised when y is allocated here."""
+    R, K = _rows(x, "qlinear_grouped")
+    if offsets.dtype != torch.int32 or offsets.numel() != E + 1:
+        raise ValueError(f"offsets must be an int32 tensor of {E + 1} elements")
+    cb, sb, _ = qlinear_packed_sizes(fmt, N, K)
+    if codes.numel() * codes.element_size() != E * cb or scales.numel() * scales.element_size() != E * sb:
+        raise ValueError(f"{E} experts of [{N}, {K}] take {E * cb} code and {E * sb} scale bytes")
+    need = qlinear_grouped_workspace_size(E, N, K, fmt, flags, R)
+    if ws is None or ws.numel() * ws.element_size() < need:
+        ws = _empty(need, x.device)
+    if y is None:
+        y = torch.empty((R, N), dtype=torch.float32, device=x.device)
+    elif y.dtype != torch.float32 or tuple(y.shape) != (R, N):
+        raise ValueError(f"y must be an fp32 tensor of shape ({R}, {N})")
+    ex = _experts_struct(E, N, K, fmt, flags, codes, scales)
+    with torch.cuda.device(x.device):
+        _check("qlinear_grouped", lib().qlinear_grouped(_ptr(x), _ptr(offsets), ctypes.byref(ex), R, _ptr(y), _ptr(ws),
+                                                        ws.numel() * ws.element_size(), _stream(stream)))
     return y
 
 
