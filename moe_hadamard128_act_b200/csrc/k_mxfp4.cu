@@ -57,6 +57,7 @@ __global__ void __launch_bounds__(kWarps * 32) k_mx_quant(const T* W, int N, int
 // expert owning every row) reads x row r, or perm[r] / topk.  A16: two E4M3 parts per value.
 template <bool A16>
 __global__ void __launch_bounds__(kWarps * 32) k_mx_act(const MxAct a) {
+    asm volatile("griddepcontrol.launch_dependents;\n" ::: "memory");  // let the product start its weight stream
     const int lane = threadIdx.x & 31;
     const int G = a.K / 128, r = blockIdx.x;
     int first = 0, count = a.R, e = 0;

@@ -42,6 +42,10 @@ inline size_t align_up(size_t v, size_t a) { return (v + a - 1) / a * a; }
 cudaError_t make_tmap_2d(const void* base, long long rows, long long width_bytes, long long ld_bytes, int box_x,
                          int box_y, int swz, CUtensorMap* out);
 
+// A TMA tensor map over packed 4-bit codes, `rows` rows of K codes (K % 128 == 0, 32-byte aligned base), box
+// [box_y rows][128 codes], each 16 codes spread over 16 bytes of shared memory (8 of them used), 128-byte swizzle.
+cudaError_t make_tmap_u4_spread(const void* base, long long rows, long long K, int box_y, CUtensorMap* out);
+
 // Per-device facts, cached on first use.
 struct DeviceInfo {
     int sm_count;
@@ -251,7 +255,7 @@ struct MxAct {
     uint8_t* scales;  // [slots][K / 128][nblk][512]
 };
 cudaError_t launch_mx_act(const MxAct& a, bool a16, cudaStream_t s);
-constexpr int kMxTokens = 64;  // rows of a token block at most
+constexpr int kMxTokens = 192;  // operand rows of a token block at most (16-bit activations: two per token)
 // Rows of a token block for this call, and the scale blocks and slots that follow from it.
 int mx_tokens(bool a16, int R, int E);
 inline int mx_nblk(bool a16, int nt) { return ((a16 ? 2 : 1) * nt + 127) / 128; }

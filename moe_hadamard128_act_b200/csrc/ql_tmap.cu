@@ -1,6 +1,7 @@
-// ql_tmap.cu -- host-side construction of TMA tensor maps for 2-D byte
-// matrices (packed weights, int8 activations), cached by (address, shape, box,
-// swizzle) since the same weight is encoded again on every call.
+// ql_tmap.cu -- host-side construction of TMA tensor maps for 2-D matrices of
+// bytes (packed weights, int8 activations) or of 4-bit codes that the copy
+// spreads to bytes, cached by (address, shape, box, swizzle, element) since the
+// same weight is encoded again on every call.
 #include <mutex>
 
 #include <cudaTypedefs.h>
@@ -14,9 +15,10 @@ struct TmapKey {
     const void* ptr;
     long long rows, width, ld;
     int box_x, box_y, swz;
+    CUtensorMapDataType type;
     bool operator==(const TmapKey& o) const {
         return ptr == o.ptr && rows == o.rows && width == o.width && ld == o.ld && box_x == o.box_x &&
-               box_y == o.box_y && swz == o.swz;
+               box_y == o.box_y && swz == o.swz && type == o.type;
     }
 };
 
@@ -26,12 +28,11 @@ CUtensorMap g_vals[128];
 int g_n = 0, g_next = 0;
 PFN_cuTensorMapEncodeTiled_v12000 g_encode = nullptr;
 
-}  // namespace
-
-cudaError_t make_tmap_2d(const void* base, long long rows, long long width_bytes, long long ld_bytes, int box_x,
-                         int box_y, int swz, CUtensorMap* out) {
+// width and box_x in elements, ld in bytes.
+cudaError_t make_tmap(const void* base, CUtensorMapDataType type, long long rows, long long width, long long ld_bytes,
+                      int box_x, int box_y, int swz, CUtensorMap* out) {
     std::lock_guard<std::mutex> lock(g_mu);
-    const TmapKey key{base, rows, width_bytes, ld_bytes, box_x, box_y, swz};
+    const TmapKey key{base, rows, width, ld_bytes, box_x, box_y, swz, type};
     for (int i = 0; i < g_n; ++i)
         if (g_keys[i] == key) {
             *out = g_vals[i];
@@ -47,12 +48,12 @@ cudaError_t make_tmap_2d(const void* base, long long rows, long long width_bytes
         }
         g_encode = reinterpret_cast<PFN_cuTensorMapEncodeTiled_v12000>(fn);
     }
-    const cuuint64_t dims[2] = {(cuuint64_t)width_bytes, (cuuint64_t)rows};
+    const cuuint64_t dims[2] = {(cuuint64_t)width, (cuuint64_t)rows};
     const cuuint64_t strides[1] = {(cuuint64_t)ld_bytes};
     const cuuint32_t box[2] = {(cuuint32_t)box_x, (cuuint32_t)box_y};
     const cuuint32_t estr[2] = {1u, 1u};
     CUtensorMap m;
-    const CUresult r = g_encode(&m, CU_TENSOR_MAP_DATA_TYPE_UINT8, 2, const_cast<void*>(base), dims, strides, box, estr,
+    const CUresult r = g_encode(&m, type, 2, const_cast<void*>(base), dims, strides, box, estr,
                                 CU_TENSOR_MAP_INTERLEAVE_NONE, static_cast<CUtensorMapSwizzle>(swz),
                                 CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
     if (r != CUDA_SUCCESS) return cudaErrorInvalidValue;
@@ -61,6 +62,18 @@ cudaError_t make_tmap_2d(const void* base, long long rows, long long width_bytes
     g_vals[slot] = m;
     *out = m;
     return cudaSuccess;
+}
+
+}  // namespace
+
+cudaError_t make_tmap_2d(const void* base, long long rows, long long width_bytes, long long ld_bytes, int box_x,
+                         int box_y, int swz, CUtensorMap* out) {
+    return make_tmap(base, CU_TENSOR_MAP_DATA_TYPE_UINT8, rows, width_bytes, ld_bytes, box_x, box_y, swz, out);
+}
+
+cudaError_t make_tmap_u4_spread(const void* base, long long rows, long long K, int box_y, CUtensorMap* out) {
+    return make_tmap(base, CU_TENSOR_MAP_DATA_TYPE_16U4_ALIGN16B, rows, K, K / 2, 128, box_y,
+                     CU_TENSOR_MAP_SWIZZLE_128B, out);
 }
 
 }  // namespace ql
