@@ -24,10 +24,9 @@
 // is, after the MMAs that read them have finished.  Two accumulators let the
 // epilogue of one tile run under the MMAs of the next.
 //
-// Warp roles: lane 0 of warp 0 brings in the weights, which wait for nothing,
-// lane 0 of warp 2 the activations, once the quantiser before this kernel is
-// done (programmatic dependent launch); lane 0 of warp 1 issues the scale
-// copies and MMAs; warps 4..7 store the sums, 32 consecutive outputs of a token
+// Warp roles: warp 0 brings in the weights, which wait for nothing, warp 2 the
+// activations, once the quantiser before this kernel is done (programmatic
+// dependent launch); warp 1 issues the scale copies and MMAs; warps 4..7 store the sums, 32 consecutive outputs of a token
 // per warp and instruction.
 //
 // All waits are bounded; on a timeout the CTA sets QL_DEVERR_TIMEOUT and winds
@@ -111,6 +110,14 @@ __device__ __forceinline__ void tmem_ld16(uint32_t addr, uint32_t r[CW]) {
 }
 __device__ __forceinline__ void tmem_wait_ld() { asm volatile("tcgen05.wait::ld.sync.aligned;\n" ::: "memory"); }
 
+// One lane of a converged warp, the same every time.
+__device__ __forceinline__ bool elect() {
+    uint32_t p;
+    asm volatile("{\n .reg .pred p;\n elect.sync _|p, 0xffffffff;\n selp.u32 %0, 1, 0, p;\n}\n" : "=r"(p));
+    return p != 0;
+}
+__device__ __forceinline__ int uniform(int v) { return __shfl_sync(kFull, v, 0); }
+
 struct Tile {
     int expert, row0, rows, wb, slot;
 };
@@ -165,7 +172,7 @@ __global__ void __launch_bounds__(kThreads, 1) k_mx_gemm(const __grid_constant__
     const MxGemm& g = p.g;
     const uint32_t base = (smem_u32(smem_raw) + 1023u) & ~1023u;
     auto bar = [&](int i) { return smem_u32(&bars[i]); };
-    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    const int warp = uniform(threadIdx.x >> 5), lane = threadIdx.x & 31;
     const int G = g.K / 128, KS = (G + KBS - 1) / KBS;
     const int nblk = g.nblk;
     // A slot: weight codes, activation codes, weight scales (KBS blocks), activation scales (KBS x nblk blocks).
@@ -214,76 +221,89 @@ __global__ void __launch_bounds__(kThreads, 1) k_mx_gemm(const __grid_constant__
     fence_before();
     __syncthreads();
     fence_after();
-    const uint32_t tmem = tmem_slot;
+    const uint32_t tmem = (uint32_t)uniform((int)tmem_slot);
     const unsigned long long lim = wait_limit(g.err);
     bool dead = false;
     Tiles tiles(g, cum);
     Tile ti;
 
-    if (warp == 0 && lane == 0) {  // ---- weights ----
-        asm volatile("prefetch.tensormap [%0];\n" ::"l"(&p.tmW) : "memory");
+    // The three issuing roles run as whole warps, with every operand the same in all lanes, and one elected lane
+    // issues: the instructions take their operands from uniform registers, which a lone lane's values would have
+    // to be moved to one by one for each of them.
+    if (warp == 0) {  // ---- weights ----
+        const bool leader = elect();
+        if (leader) asm volatile("prefetch.tensormap [%0];\n" ::"l"(&p.tmW) : "memory");
         const int NB = (g.N + TM - 1) / TM;
         int step = 0, s = 0, ph = 1;
         while (!dead && tiles.next(ti)) {
-            const int row = ti.expert * g.N + ti.wb * TM;
-            const uint8_t* sf = g.scales + ((long long)ti.expert * NB + ti.wb) * G * 512;
+            const int expert = uniform(ti.expert), wb = uniform(ti.wb);
+            const int row = expert * g.N + wb * TM;
+            const uint8_t* sf = g.scales + ((long long)expert * NB + wb) * G * 512;
             for (int k = 0; k < KS; ++k, ++step) {
-                if (!mbar_wait(bar(B_EMPTY + s), ph, lim)) {
+                if (!__all_sync(kFull, mbar_wait(bar(B_EMPTY + s), ph, lim))) {
                     dead = true;
                     break;
                 }
                 const unsigned sfb = min(KBS, G - k * KBS) * 512;
                 const uint32_t slot = base + s * p.stage_bytes, fb = bar(B_FULL + s);
-                mbar_expect_tx(fb, (A16 ? A_BYTES / 2 : A_BYTES) + sfb);  // spread copies count the packed bytes
-                tma_load_2d(slot, &p.tmW, k * 128, row, fb);
-                bulk_load(slot + sa_off, sf + (long long)k * KBS * 512, sfb, fb);
+                if (leader) {
+                    mbar_expect_tx(fb, (A16 ? A_BYTES / 2 : A_BYTES) + sfb);  // spread copies count the packed bytes
+                    tma_load_2d(slot, &p.tmW, k * 128, row, fb);
+                    bulk_load(slot + sa_off, sf + (long long)k * KBS * 512, sfb, fb);
+                }
                 if (++s == p.stages) { s = 0; ph ^= 1; }
             }
         }
         // Copies still in flight must land before the CTA's shared memory is released.  A slot's phase also
         // takes the other producer's arrival: if that one gave up, this wait ends at its bound.
         for (int j = step > p.stages ? step - p.stages : 0; j < step; ++j)
-            if (!mbar_wait(bar(B_FULL + j % p.stages), (j / p.stages) & 1)) break;
-    } else if (warp == 2 && lane == 0) {  // ---- activations ----
-        asm volatile("prefetch.tensormap [%0];\n" ::"l"(&p.tmX) : "memory");
-        asm volatile("prefetch.tensormap [%0];\n" ::"l"(&p.tmXb) : "memory");
+            if (!__all_sync(kFull, mbar_wait(bar(B_FULL + j % p.stages), (j / p.stages) & 1))) break;
+    } else if (warp == 2) {  // ---- activations ----
+        const bool leader = elect();
+        if (leader) {
+            asm volatile("prefetch.tensormap [%0];\n" ::"l"(&p.tmX) : "memory");
+            asm volatile("prefetch.tensormap [%0];\n" ::"l"(&p.tmXb) : "memory");
+        }
         asm volatile("griddepcontrol.wait;\n" ::: "memory");  // the quantiser's codes and scales
         int step = 0, s = 0, ph = 1;
         while (!dead && tiles.next(ti)) {
-            const int n16 = mx_pad16(ti.rows);
-            const uint8_t* sf = g.xs + (long long)ti.slot * G * nblk * 512;
+            const int n16 = uniform(mx_pad16(ti.rows)), row0 = uniform(ti.row0);
+            const uint8_t* sf = g.xs + (long long)uniform(ti.slot) * G * nblk * 512;
             for (int k = 0; k < KS; ++k, ++step) {
-                if (!mbar_wait(bar(B_EMPTY + s), ph, lim)) {
+                if (!__all_sync(kFull, mbar_wait(bar(B_EMPTY + s), ph, lim))) {
                     dead = true;
                     break;
                 }
                 const unsigned sfb = min(KBS, G - k * KBS) * nblk * 512;
                 const uint32_t slot = base + s * p.stage_bytes, fb = bar(B_FULL + s);
-                mbar_expect_tx(fb, P * n16 * 128 + sfb);
-                for (int pl = 0; pl < P; ++pl) {
-                    const int row = pl * g.R + ti.row0;
-                    const uint32_t dst = slot + b_off + pl * n16 * 128;
-                    int r = 0;
-                    for (; r + BIG <= n16; r += BIG) tma_load_2d(dst + r * 128, &p.tmXb, k * 128, row + r, fb);
-                    for (; r < n16; r += SMALL) tma_load_2d(dst + r * 128, &p.tmX, k * 128, row + r, fb);
+                if (leader) {
+                    mbar_expect_tx(fb, P * n16 * 128 + sfb);
+                    for (int pl = 0; pl < P; ++pl) {
+                        const int row = pl * g.R + row0;
+                        const uint32_t dst = slot + b_off + pl * n16 * 128;
+                        int r = 0;
+                        for (; r + BIG <= n16; r += BIG) tma_load_2d(dst + r * 128, &p.tmXb, k * 128, row + r, fb);
+                        for (; r < n16; r += SMALL) tma_load_2d(dst + r * 128, &p.tmX, k * 128, row + r, fb);
+                    }
+                    bulk_load(slot + sb_off, sf + (long long)k * KBS * nblk * 512, sfb, fb);
                 }
-                bulk_load(slot + sb_off, sf + (long long)k * KBS * nblk * 512, sfb, fb);
                 if (++s == p.stages) { s = 0; ph ^= 1; }
             }
         }
         for (int j = step > p.stages ? step - p.stages : 0; j < step; ++j)
-            if (!mbar_wait(bar(B_FULL + j % p.stages), (j / p.stages) & 1)) break;
-    } else if (warp == 1 && lane == 0) {  // ---- scale copies and MMAs ----
+            if (!__all_sync(kFull, mbar_wait(bar(B_FULL + j % p.stages), (j / p.stages) & 1))) break;
+    } else if (warp == 1) {  // ---- scale copies and MMAs ----
+        const bool leader = elect();
         int s = 0, ph = 0, tl = 0;
         while (!dead && tiles.next(ti)) {
             const int b = tl & 1;
-            if (!mbar_wait(bar(B_ACCE + b), ((tl >> 1) & 1) ^ 1, lim)) {  // the epilogue is done with it
+            if (!__all_sync(kFull, mbar_wait(bar(B_ACCE + b), ((tl >> 1) & 1) ^ 1, lim))) {  // the epilogue is done
                 dead = true;
                 break;
             }
-            const uint32_t d = tmem + b * p.acc_cols, id0 = idesc<A16>(P * mx_pad16(ti.rows));
+            const uint32_t d = tmem + b * p.acc_cols, id0 = idesc<A16>(P * uniform(mx_pad16(ti.rows)));
             for (int k = 0; k < KS; ++k) {
-                if (!mbar_wait(bar(B_FULL + s), ph, lim)) {
+                if (!__all_sync(kFull, mbar_wait(bar(B_FULL + s), ph, lim))) {
                     dead = true;
                     break;
                 }
@@ -291,26 +311,36 @@ __global__ void __launch_bounds__(kThreads, 1) k_mx_gemm(const __grid_constant__
                 const uint32_t slot = base + s * p.stage_bytes, sf = tmem + p.sf0 + s * p.sf_cols;
                 const uint32_t sfb = sf + 4 * KBS;
                 const int kbs = min(KBS, G - k * KBS);
-                for (int q = 0; q < kbs; ++q) copy_scales(sf + 4 * q, desc_scales(slot + sa_off + q * 512));
-                for (int q = 0; q < kbs * nblk; ++q) copy_scales(sfb + 4 * q, desc_scales(slot + sb_off + q * 512));
                 const uint64_t ad = desc_sw128(slot), bd = desc_sw128(slot + b_off);
+                const uint64_t sad = desc_scales(slot + sa_off), sbd = desc_scales(slot + sb_off);
+                if (leader) {
 #pragma unroll
-                for (int j = 0; j < 4; ++j) {  // 32 bytes of every row: +2 in the descriptors' address field
-                    const int q = A16 ? 0 : j >> 1, byte = A16 ? j : 2 * (j & 1);  // its scales' block and byte
-                    if (q < kbs)
-                        mma<A16>(d, ad + 2 * j, bd + 2 * j, id0 | (uint32_t)byte << 4 | (uint32_t)byte << 29, sf + 4 * q,
-                                 sfb + 4 * nblk * q, (k | j) ? 1u : 0u);
+                    for (int q = 0; q < KBS; ++q) {  // 512 bytes a copy: +32 in the descriptors' address field
+                        if (q < kbs) {
+                            copy_scales(sf + 4 * q, sad + 32 * q);
+                            copy_scales(sfb + 4 * nblk * q, sbd + 32 * nblk * q);
+                            if (nblk > 1) copy_scales(sfb + 4 * (nblk * q + 1), sbd + 32 * (nblk * q + 1));
+                        }
+                    }
+#pragma unroll
+                    for (int j = 0; j < 4; ++j) {  // 32 bytes of every row: +2 in the descriptors' address field
+                        const int q = A16 ? 0 : j >> 1, byte = A16 ? j : 2 * (j & 1);  // its scales' block and byte
+                        if (q < kbs)
+                            mma<A16>(d, ad + 2 * j, bd + 2 * j, id0 | (uint32_t)byte << 4 | (uint32_t)byte << 29,
+                                     sf + 4 * q, sfb + 4 * nblk * q, (k | j) ? 1u : 0u);
+                    }
+                    commit(bar(B_EMPTY + s));  // the slot and its scale columns may be refilled once these are done
                 }
-                commit(bar(B_EMPTY + s));  // the slot and its scale columns may be refilled once these are done
+                __syncwarp();
                 if (++s == p.stages) { s = 0; ph ^= 1; }
             }
             if (dead) break;
-            commit(bar(B_ACCF + b));
+            if (leader) commit(bar(B_ACCF + b));
             ++tl;
         }
         // Every MMA issued must finish before tensor memory is freed.
-        commit(bar(B_DRAIN));
-        mbar_wait(bar(B_DRAIN), 0);
+        if (leader) commit(bar(B_DRAIN));
+        __all_sync(kFull, mbar_wait(bar(B_DRAIN), 0));
     } else if (warp >= kEpiWarp0) {  // ---- epilogue ----
         const int q = warp & 3;
         int tl = 0;
