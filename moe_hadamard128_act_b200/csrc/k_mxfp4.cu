@@ -2,11 +2,11 @@
 // weights and activations, the packer of given codes, and the values that
 // packed codes stand for.
 //
-// One warp takes one row's 128 columns, 4 neighbouring values a lane, as the
-// other quantisers of this library do: the rotation's shuffles stay inside the
-// warp, a 32-block is 8 lanes, and the 128 columns' four scale bytes are one
-// word of the scale layout (mx_layout.cuh).  Bound by HBM: 2 (bf16) or 4 (fp32)
-// bytes in and 17/32 byte out per value.
+// Half a warp takes one row's 128 columns, 8 neighbouring values a lane (one
+// 16-byte load of bf16): the rotation's shuffles stay inside the half warp, a
+// 32-block is 4 lanes, and the 128 columns' four scale bytes are one word of
+// the scale layout (mx_layout.cuh).  Bound by HBM: 2 (bf16) or 4 (fp32) bytes in
+// and 17/32 byte out per value.
 #include "mx_layout.cuh"
 #include "ql_internal.h"
 
@@ -15,95 +15,176 @@ namespace {
 
 constexpr int kWarps = 8;
 
-__device__ __forceinline__ void load4(const float* p, float v[4]) {
-    const float4 r = __ldg(reinterpret_cast<const float4*>(p));
-    v[0] = r.x; v[1] = r.y; v[2] = r.z; v[3] = r.w;
+__device__ __forceinline__ void load8(const float* p, float v[8]) {
+    const float4 a = __ldg(reinterpret_cast<const float4*>(p)), b = __ldg(reinterpret_cast<const float4*>(p) + 1);
+    v[0] = a.x; v[1] = a.y; v[2] = a.z; v[3] = a.w;
+    v[4] = b.x; v[5] = b.y; v[6] = b.z; v[7] = b.w;
 }
-__device__ __forceinline__ void load4(const __nv_bfloat16* p, float v[4]) { load4_bf16(p, v); }
-
-// The warp's four scale bytes (one per 8 lanes) as the word that lane 0 stores.
-__device__ __forceinline__ uint32_t scale_word(uint32_t byte) {
-    uint32_t w = byte;
+__device__ __forceinline__ void load8(const __nv_bfloat16* p, float v[8]) {
+    const uint4 r = __ldg(reinterpret_cast<const uint4*>(p));
+    const uint32_t w[4] = {r.x, r.y, r.z, r.w};
 #pragma unroll
-    for (int b = 1; b < 4; ++b) w |= __shfl_sync(kFull, byte, 8 * b) << (8 * b);
-    return w;
+    for (int i = 0; i < 4; ++i) {
+        v[2 * i] = __uint_as_float(w[i] << 16);
+        v[2 * i + 1] = __uint_as_float(w[i] & 0xFFFF0000u);
+    }
 }
 
-// Rows [0, N) of W to packed MXFP4; rows up to the next multiple of 128 get zero scales.
+// Rows [0, N) of W to packed MXFP4; rows up to the next multiple of 128 get zero scales.  A CTA takes kRows
+// rows and walks them 128 columns a half warp at a time, all rows' loads of a column first.
+constexpr int kRows = 4;
 template <typename T>
 __global__ void __launch_bounds__(kWarps * 32) k_mx_quant(const T* W, int N, int K, int rotate, uint8_t* codes,
                                                           uint8_t* scales) {
-    const int lane = threadIdx.x & 31;
-    const int G = K / 128;
-    const long long units = (long long)((N + 127) / 128 * 128) * G;
-    const long long nw = (long long)gridDim.x * kWarps;
-    for (long long u = (long long)blockIdx.x * kWarps + (threadIdx.x >> 5); u < units; u += nw) {
-        const int r = (int)(u / G), g = (int)(u - (long long)r * G);
-        uint32_t word = 0;
-        if (r < N) {
-            float v[4];
-            load4(W + (long long)r * K + g * 128 + 4 * lane, v);
-            if (rotate) fwht128_warp(v, lane);
+    const int lane = threadIdx.x & 15, G = K / 128;
+    const int r0 = blockIdx.x * kRows;
+    // every lane of a warp goes through the same iterations (the shuffles want both halves)
+    for (int g0 = (blockIdx.y * kWarps + (threadIdx.x >> 5)) * 2; g0 < G; g0 += gridDim.y * kWarps * 2) {
+        const int g = g0 + ((threadIdx.x >> 4) & 1);
+        const int gl = min(g, G - 1);
+        float v[kRows][8];
+#pragma unroll
+        for (int i = 0; i < kRows; ++i) load8(W + (long long)min(r0 + i, N - 1) * K + gl * 128 + 8 * lane, v[i]);
+#pragma unroll
+        for (int i = 0; i < kRows; ++i) {
+            const int r = r0 + i;
+            if (rotate) mx_fwht128(v[i], lane);
             uint32_t byte;
-            const uint32_t c = mx_quant4(v, byte);
-            *reinterpret_cast<uint16_t*>(codes + (long long)r * (K / 2) + g * 64 + 2 * lane) = (uint16_t)c;
-            word = scale_word(byte);
+            const uint32_t c = mx_quant8(v[i], byte);
+            uint32_t word = mx_scale_word(byte, lane);
+            if (g >= G) continue;
+            if (r < N) *reinterpret_cast<uint32_t*>(codes + (long long)r * (K / 2) + g * 64 + 4 * lane) = c;
+            else word = 0;
+            if (lane == 0) *reinterpret_cast<uint32_t*>(scales + mx_scale_at(r >> 7, G, g, 1, r & 127)) = word;
         }
-        if (lane == 0) *reinterpret_cast<uint32_t*>(scales + mx_scale_at(r >> 7, G, g, 1, r & 127)) = word;
     }
 }
 
-// Activations into the order of the product's tiles (mx_layout.cuh): sorted row r of `offsets` (null: one
-// expert owning every row) reads x row r, or perm[r] / topk.  A16: two E4M3 parts per value.
-template <bool A16>
+// Activations into the order of the product's tiles (mx_layout.cuh).  A CTA takes 128-column units of one row
+// of x, quantised once and written to every place that the row has among the sorted rows: its own (offsets
+// null, or sorted rows given), or one for each of the token's topk pairs, at the pair's position inv[] in its
+// expert's segment.
+struct Place {
+    long long slot;
+    int row, c, low;  // sorted row (-1: none), token of its block, operand row of its low part
+    long long y;      // output row
+};
+
+// Digits: 32, and a factor of 2^-32 on the row's sums, if no magnitude of the row (rotated and rounded as the
+// quantiser sees it) reaches 2^-64, else 0; by a whole warp.  The digits' scales end at 2^-127, which cuts a
+// block below 2^-105; beside a value of 2^-64 that is at most 2^-65 of it, and without one the row is moved up.
+constexpr uint32_t kSmallRow = 63u << 23;  // 2^-64
+__device__ __noinline__ int row_up(const __nv_bfloat16* x, int G, int rotate) {
+    const int lane = threadIdx.x & 15;
+    uint32_t m = 0;
+    for (int g0 = 0; g0 < G; g0 += 2) {
+        float v[8];
+        load8(x + min(g0 + (int)((threadIdx.x >> 4) & 1), G - 1) * 128 + 8 * lane, v);
+        if (rotate) mx_fwht128(v, lane);
+#pragma unroll
+        for (int i = 0; i < 8; ++i) v[i] = __bfloat162float(__float2bfloat16_rn(v[i]));
+#pragma unroll
+        for (int i = 0; i < 8; ++i) m = max(m, __float_as_uint(v[i]) & 0x7FFFFFFFu);
+    }
+    return __reduce_max_sync(kFull, m) < kSmallRow ? 32 : 0;
+}
+
+template <int MODE>
 __global__ void __launch_bounds__(kWarps * 32) k_mx_act(const MxAct a) {
     asm volatile("griddepcontrol.launch_dependents;\n" ::: "memory");  // let the product start its weight stream
-    const int lane = threadIdx.x & 31;
-    const int G = a.K / 128, r = blockIdx.x;
-    int first = 0, count = a.R, e = 0;
-    if (a.offsets) {
-        e = mx_warp_search(a.E, r, [&](int i) { return __ldg(a.offsets + i); });
-        if (e < 0) return;
-        int end;
-        mx_segment(a.offsets, e, a.R, first, end);
-        if (r < first || r >= end) return;  // a row of no expert
-        count = end - first;
+    __shared__ Place places[kMxTopk];
+    const int G = a.K / 128, x = blockIdx.x, nt = a.plan.nt, nblk = a.plan.nblk;
+    const int dests = a.ids ? a.topk : 1;
+    for (int j = threadIdx.x >> 5; j < dests; j += kWarps) {
+        const long long y = a.ids ? (long long)x * a.topk + j : x;
+        int r = x, e = 0, first = 0, end = a.R;
+        if (a.ids) {
+            r = __ldg(a.inv + y);
+            e = __ldg(a.ids + y);
+            if (e < 0 || e >= a.E || r < 0 || r >= a.R) r = -1;
+        } else if (a.offsets) {
+            e = mx_warp_search(a.E, r, [&](int i) { return __ldg(a.offsets + i); });
+            if (e < 0) r = -1;
+        }
+        if (a.offsets && r >= 0) {
+            mx_segment(a.offsets, e, a.R, first, end);
+            if (r < first || r >= end) r = -1;  // a row of no expert
+        }
+        const int i = r < 0 ? 0 : (r - first) / nt, c = r < 0 ? 0 : (r - first) - i * nt;
+        if ((threadIdx.x & 31) == 0)
+            places[j] = Place{first / nt + e + i, r, c, mx_pad16(min(nt, end - first - i * nt)) + c, y};
     }
-    long long src = r;
-    if (a.perm) {
-        const int p = __ldg(a.perm + r);
-        if (p < 0 || p >= a.R) return;
-        src = p / a.topk;
+    __syncthreads();
+    if (dests == 1 && places[0].row < 0) return;
+    if (a.plan.split) {  // the product adds into these rows
+        for (int j = 0; j < dests; ++j) {
+            if (places[j].row < 0) continue;
+            float* const y = a.y + places[j].y * a.N;
+            for (int n = blockIdx.y * blockDim.x + threadIdx.x; n < a.N; n += gridDim.y * blockDim.x) y[n] = 0.0f;
+        }
     }
-    const int i = (r - first) / a.nt, c = (r - first) - i * a.nt;
-    const int rows = min(a.nt, count - i * a.nt);
-    const long long slot = first / a.nt + e + i;
-    for (int g = blockIdx.y * kWarps + (threadIdx.x >> 5); g < G; g += gridDim.y * kWarps) {
-        float v[4];
-        load4_bf16(a.x + src * a.K + g * 128 + 4 * lane, v);
-        if (a.rotate) fwht128_warp(v, lane);
-        uint32_t byte;
-        if constexpr (A16) {
-            if (a.rotate) {
+    const int lane = threadIdx.x & 15;
+    const __nv_bfloat16* const xr = a.x + (long long)x * a.K;
+    for (int g0 = (blockIdx.y * kWarps + (threadIdx.x >> 5)) * 2; g0 < G; g0 += gridDim.y * kWarps * 2) {
+        const int g = g0 + ((threadIdx.x >> 4) & 1);
+        float v[8];
+        load8(xr + min(g, G - 1) * 128 + 8 * lane, v);
+        if (a.rotate) {
+            mx_fwht128(v, lane);
+            if constexpr (MODE != kMxA4) {
 #pragma unroll
-                for (int k = 0; k < 4; ++k) v[k] = __bfloat162float(__float2bfloat16_rn(v[k]));
+                for (int k = 0; k < 8; ++k) v[k] = __bfloat162float(__float2bfloat16_rn(v[k]));
             }
-            uint32_t hi, lo;
-            mx_split4(v, hi, lo, byte);
-            const long long at = (long long)r * a.K + g * 128 + 4 * lane;
-            *reinterpret_cast<uint32_t*>(a.codes + at) = hi;
-            *reinterpret_cast<uint32_t*>(a.codes + (long long)a.R * a.K + at) = lo;
-            const uint32_t word = scale_word(byte);
-            const uint32_t low = scale_word(byte == 255 ? 255 : byte - 5);
-            if (lane == 0) {
-                *reinterpret_cast<uint32_t*>(a.scales + mx_scale_at(slot, G, g, a.nblk, c)) = word;
-                *reinterpret_cast<uint32_t*>(a.scales + mx_scale_at(slot, G, g, a.nblk, mx_pad16(rows) + c)) = low;
-            }
+        }
+        uint32_t byte, c = 0, d[8];
+        uint2 hi, lo;
+        if constexpr (MODE == kMxA4) {
+            c = mx_quant8(v, byte);
+        } else if constexpr (MODE == kMxParts) {
+            mx_split8(v, hi, lo, byte);
         } else {
-            const uint32_t q = mx_quant4(v, byte);
-            *reinterpret_cast<uint16_t*>(a.codes + (long long)r * (a.K / 2) + g * 64 + 2 * lane) = (uint16_t)q;
-            const uint32_t word = scale_word(byte);
-            if (lane == 0) *reinterpret_cast<uint32_t*>(a.scales + mx_scale_at(slot, G, g, a.nblk, c)) = word;
+            const uint32_t m = mx_block_max(v);
+            // Blocks of ordinary size settle that the row is not a small one; zeros fit any factor.  The row's
+            // first block answers for the row, whatever it holds.
+            int up = 0;
+            if (__any_sync(kFull, m < kSmallRow && (m || g0 == 0))) up = row_up(xr, G, a.rotate);
+            if (g0 == 0 && (threadIdx.x & 31) == 0)
+                for (int j = 0; j < dests; ++j)
+                    if (places[j].row >= 0) a.factors[places[j].row] = up ? 0x1p-32f : 1.0f;
+            mx_digits8(v, m >> 23, up, d, byte);
+        }
+        const uint32_t word = mx_scale_word(byte, lane);
+        const uint32_t lword = MODE == kMxParts ? mx_scale_word(byte == 255 ? 255u : byte - 5u, lane) : 0u;
+        uint32_t dword = 0;  // digits: lane p < 8 holds digit p's four scales, each 3 p below the first's
+        if constexpr (MODE == kMxDigits) {
+#pragma unroll
+            for (int k = 0; k < 4; ++k) {
+                const uint32_t w = (word >> (8 * k)) & 0xFFu;
+                dword |= (w == 255 ? 255u : w - 3u * (lane & 7)) << (8 * k);
+            }
+        }
+        if (g >= G) continue;
+        for (int j = 0; j < dests; ++j) {
+            const Place p = places[j];
+            if (p.row < 0) continue;
+            auto scale = [&](int r, uint32_t w) {
+                *reinterpret_cast<uint32_t*>(a.scales + mx_scale_at(p.slot, G, g, nblk, r)) = w;
+            };
+            if constexpr (MODE == kMxA4) {
+                *reinterpret_cast<uint32_t*>(a.codes + (long long)p.row * (a.K / 2) + g * 64 + 4 * lane) = c;
+                if (lane == 0) scale(p.c, word);
+            } else if constexpr (MODE == kMxParts) {
+                const long long at = (long long)p.row * a.K + g * 128 + 8 * lane;
+                *reinterpret_cast<uint2*>(a.codes + at) = hi;
+                *reinterpret_cast<uint2*>(a.codes + (long long)a.R * a.K + at) = lo;
+                if (lane == 0) scale(p.c, word);
+                if (lane == 1) scale(p.low, lword);
+            } else {
+#pragma unroll
+                for (int k = 0; k < 8; ++k)
+                    *reinterpret_cast<uint32_t*>(a.codes + (8LL * p.row + k) * (a.K / 2) + g * 64 + 4 * lane) = d[k];
+                if (lane < 8) scale(8 * p.c + lane, dword);
+            }
         }
     }
 }
@@ -135,33 +216,41 @@ __global__ void __launch_bounds__(256) k_mx_pack_scales(const uint8_t* in, int N
         r < N ? __ldg(reinterpret_cast<const uint32_t*>(in) + u) : 0u;
 }
 
-// 8 codes a thread: 4 bytes in, 16 bytes of bf16 out.  The f16 value of a code times a power of two has two
-// significant bits, so the fp32 product and its rounding to bf16 are exact.
-__global__ void __launch_bounds__(256) k_mx_dequant(const uint8_t* codes, const uint8_t* scales, int K, long long n8,
+// 8 codes of kRows rows a thread: 4 bytes in, 16 bytes of bf16 out.  The f16 value of a code times a power of
+// two has two significant bits, so the fp32 product and its rounding to bf16 are exact.
+__global__ void __launch_bounds__(256) k_mx_dequant(const uint8_t* codes, const uint8_t* scales, int N, int K,
                                                     __nv_bfloat16* out) {
-    const long long i = (long long)blockIdx.x * blockDim.x + threadIdx.x;
-    if (i >= n8) return;
-    const int per = K / 8;
-    const int r = (int)(i / per), k = (int)(i - (long long)r * per) * 8;
-    const uint32_t w = __ldg(reinterpret_cast<const uint32_t*>(codes) + i);
-    const float s = mx_scale(__ldg(scales + mx_scale_at(r >> 7, K / 128, k >> 7, 1, r & 127) + ((k >> 5) & 3)));
-    uint32_t o[4];
+    const int r0 = blockIdx.x * kRows, G = K / 128;
+    for (int u = threadIdx.x; u < K / 8; u += 256) {
+        uint32_t w[kRows], b[kRows];
 #pragma unroll
-    for (int j = 0; j < 4; ++j) {
-        const uint32_t h = e2m1x2_to_f16x2((w >> (8 * j)) & 0xFFu);
-        const __nv_bfloat162 b = __floats2bfloat162_rn(f16_bits_to_float((uint16_t)h) * s,
-                                                       f16_bits_to_float((uint16_t)(h >> 16)) * s);
-        o[j] = *reinterpret_cast<const uint32_t*>(&b);
+        for (int i = 0; i < kRows; ++i) {
+            const int r = min(r0 + i, N - 1);
+            w[i] = __ldg(reinterpret_cast<const uint32_t*>(codes + (long long)r * (K / 2)) + u);
+            b[i] = __ldg(scales + mx_scale_at(r >> 7, G, u >> 4, 1, r & 127) + ((u >> 2) & 3));
+        }
+#pragma unroll
+        for (int i = 0; i < kRows; ++i) {
+            const float s = mx_scale(b[i]);
+            uint32_t o[4];
+#pragma unroll
+            for (int j = 0; j < 4; ++j) {
+                const uint32_t h = e2m1x2_to_f16x2((w[i] >> (8 * j)) & 0xFFu);
+                const __nv_bfloat162 p = __floats2bfloat162_rn(f16_bits_to_float((uint16_t)h) * s,
+                                                               f16_bits_to_float((uint16_t)(h >> 16)) * s);
+                o[j] = *reinterpret_cast<const uint32_t*>(&p);
+            }
+            if (r0 + i < N)
+                reinterpret_cast<uint4*>(out + (long long)(r0 + i) * K)[u] = make_uint4(o[0], o[1], o[2], o[3]);
+        }
     }
-    reinterpret_cast<uint4*>(out)[i] = make_uint4(o[0], o[1], o[2], o[3]);
 }
 
 template <typename T>
 cudaError_t quant(const T* W, int N, int K, int rotate, uint8_t* codes, uint8_t* scales, cudaStream_t s) {
-    const long long units = (long long)((N + 127) / 128 * 128) * (K / 128);
-    const long long blocks = (units + kWarps - 1) / kWarps;
-    k_mx_quant<T><<<(unsigned)(blocks < 148 * 64 ? blocks : 148 * 64), kWarps * 32, 0, s>>>(W, N, K, rotate, codes,
-                                                                                          scales);
+    const int blocks = (N + 127) / 128 * (128 / kRows), passes = (K / 128 + 2 * kWarps - 1) / (2 * kWarps);
+    const dim3 grid((unsigned)blocks, (unsigned)(blocks < 148 ? passes : 1));  // few rows: cut along K too
+    k_mx_quant<T><<<grid, kWarps * 32, 0, s>>>(W, N, K, rotate, codes, scales);
     return cudaGetLastError();
 }
 
@@ -176,10 +265,15 @@ cudaError_t launch_mx_quant_rows(const void* x, int M, int K, int rotate, uint8_
     return quant(static_cast<const __nv_bfloat16*>(x), M, K, rotate, codes, scales, s);
 }
 
-cudaError_t launch_mx_act(const MxAct& a, bool a16, cudaStream_t s) {
-    const dim3 grid((unsigned)a.R, (unsigned)((a.K / 128 + kWarps - 1) / kWarps));
-    if (a16) k_mx_act<true><<<grid, kWarps * 32, 0, s>>>(a);
-    else k_mx_act<false><<<grid, kWarps * 32, 0, s>>>(a);
+cudaError_t launch_mx_act(const MxAct& a, cudaStream_t s) {
+    // One CTA a row; few rows are cut along K instead, so that their columns are not walked one after another.
+    const int rows = a.ids ? a.R / a.topk : a.R, passes = (a.K / 128 + 2 * kWarps - 1) / (2 * kWarps);
+    const dim3 grid((unsigned)rows, (unsigned)(rows < 148 ? passes : 1));
+    switch (a.plan.mode) {
+    case kMxA4: k_mx_act<kMxA4><<<grid, kWarps * 32, 0, s>>>(a); break;
+    case kMxDigits: k_mx_act<kMxDigits><<<grid, kWarps * 32, 0, s>>>(a); break;
+    default: k_mx_act<kMxParts><<<grid, kWarps * 32, 0, s>>>(a);
+    }
     return cudaGetLastError();
 }
 
@@ -193,8 +287,8 @@ cudaError_t launch_mx_pack(const uint8_t* codes_in, const uint8_t* scales_in, in
 }
 
 cudaError_t launch_mx_dequant(const uint8_t* codes, const uint8_t* scales, int N, int K, void* out, cudaStream_t s) {
-    const long long n8 = (long long)N * (K / 8);
-    k_mx_dequant<<<(unsigned)((n8 + 255) / 256), 256, 0, s>>>(codes, scales, K, n8, static_cast<__nv_bfloat16*>(out));
+    k_mx_dequant<<<(unsigned)((N + kRows - 1) / kRows), 256, 0, s>>>(codes, scales, N, K,
+                                                                   static_cast<__nv_bfloat16*>(out));
     return cudaGetLastError();
 }
 

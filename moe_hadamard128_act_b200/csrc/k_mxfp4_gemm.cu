@@ -7,22 +7,34 @@
 // from tensor memory, so nothing is dequantised and one fp32 accumulator takes
 // the whole K.
 //   4-bit activations (kind::mxf4): both operands packed E2M1, K = 64 a step.
-//   16-bit activations (kind::mxf8f6f4): the weights' codes are spread to bytes
-//     by the copy engine (16 codes to 16 bytes) on their way into shared memory,
-//     and x enters as two E4M3 parts with scales of their own, x = hi + lo, the
-//     low parts being further operand rows: column c of the accumulator is the
-//     high part's sum of token c, column n16 + c the low part's, and the
-//     epilogue adds them.  A weight tile is thus read once for both.
+//   16-bit activations, few rows (kind::mxf4): a token enters as eight rows of
+//     E2M1 digits in base 8, each with scales of its own, whose products the
+//     epilogue adds up.  The weights stream as fast as with 4-bit activations.
+//   16-bit activations, many rows (kind::mxf8f6f4): the weights' codes are
+//     spread to bytes by the copy engine (16 codes to 16 bytes) on their way into
+//     shared memory, and x enters as two E4M3 parts with scales of their own,
+//     x = hi + lo, the low parts being further operand rows: column c of the
+//     accumulator is the high part's sum of token c, column n16 + c the low
+//     part's, and the epilogue adds them.  A quarter of the digits' tensor work
+//     at half its rate, but the spreading copy brings only half as many codes a
+//     second, which is what few rows wait for.
 //
 // A tile is 128 weight rows (the MMA's M, tensor-memory lanes) by one token
-// block (its N: the block's rows rounded up to 16, for each part), so a decode
-// batch and a prefill differ in N alone.  A step is 128 bytes of every operand
+// block (its N: the block's operand rows rounded up to 16), so a decode batch and
+// a prefill differ in N alone.  A step is 128 bytes of every operand
 // row: 256 columns of K, or 128.  A ring slot holds the step's weight codes
 // (16 KB), its activation codes and both scale blocks; as many slots as shared
 // and tensor memory allow keep the weights streaming.  Each slot has its own
 // tensor-memory columns for its scales: they are rewritten only when the slot
 // is, after the MMAs that read them have finished.  Two accumulators let the
 // epilogue of one tile run under the MMAs of the next.
+//
+// With few tiles the sums of a tile may be cut along K between two CTAs
+// (MxPlan::split): the work is one row of steps, tile after tile, dealt out in
+// equal runs, none shorter than a tile or else exactly half of one, so that at
+// most two CTAs meet in a tile.  Both add into y, which the quantiser zeroed:
+// 0 + a + b is the same in either order, so the result does not depend on which
+// comes first.
 //
 // Warp roles: warp 0 brings in the weights, which wait for nothing, warp 2 the
 // activations, once the quantiser before this kernel is done (programmatic
@@ -54,7 +66,7 @@ struct MxParams {
     CUtensorMap tmW;         // weight codes: [E * N rows], box [128 rows][128 bytes of shared memory]
     CUtensorMap tmX, tmXb;   // activation codes: [R or 2 R rows], boxes of 16 and 64 rows x 128 bytes
     MxGemm g;
-    int stages, stage_bytes;  // ring
+    int stages, stage_bytes;     // ring
     int acc_cols, sf0, sf_cols;  // tensor memory: accumulator stride, first scale column, scale columns per slot
 };
 
@@ -68,15 +80,15 @@ __device__ __forceinline__ uint64_t desc_scales(uint32_t addr) {
 }
 // Block-scaled kinds: A format at bits 7-9, B format at 10-12, N >> 3 at 17-22, scales UE8M0 (bit 23), M >> 7 at
 // 27-28; the scales' byte within a tensor-memory word at 4-5 (B) and 29-30 (A).
-template <bool A16>
+template <int MODE>
 __device__ __forceinline__ uint32_t idesc(int n) {
-    const uint32_t fmt = A16 ? (5u << 7) : (1u << 7) | (1u << 10);  // E2M1 x E4M3, or E2M1 x E2M1
+    const uint32_t fmt = MODE == kMxParts ? (5u << 7) : (1u << 7) | (1u << 10);  // E2M1 x E4M3, or E2M1 x E2M1
     return fmt | ((uint32_t)(n >> 3) << 17) | (1u << 23) | ((uint32_t)(TM >> 7) << 27);
 }
-template <bool A16>
+template <int MODE>
 __device__ __forceinline__ void mma(uint32_t d, uint64_t ad, uint64_t bd, uint32_t id, uint32_t sfa, uint32_t sfb,
                                     uint32_t acc_in) {
-    if constexpr (A16)
+    if constexpr (MODE == kMxParts)
         asm volatile(
             "{\n .reg .pred p;\n setp.ne.b32 p, %6, 0;\n"
             " tcgen05.mma.cta_group::1.kind::mxf8f6f4.block_scale.scale_vec::1X [%0], %1, %2, %3, [%4], [%5], p;\n}\n" ::"r"(d),
@@ -118,63 +130,91 @@ __device__ __forceinline__ bool elect() {
 }
 __device__ __forceinline__ int uniform(int v) { return __shfl_sync(kFull, v, 0); }
 
+// Accumulator columns of a block of `rows` tokens.
+template <int MODE>
+__device__ __forceinline__ int columns(int rows) {
+    return MODE == kMxParts ? 2 * mx_pad16(rows) : mx_pad16(mx_planes(MODE) * rows);
+}
+
 struct Tile {
     int expert, row0, rows, wb, slot;
+    int k0, k1;  // its steps
 };
 
-// The CTA's tiles, each role walking the same list: tile t of all, weight block by weight block within an
-// expert so that its token blocks share the weights in L2.  cum[e]: token blocks of the experts before e.
+// The CTA's tiles, each role walking the same list: weight block by weight block within an expert so that its
+// token blocks share the weights in L2; cum[e]: token blocks of the experts before e.
 struct Tiles {
     const MxGemm& g;
     const int* cum;
-    int NB, total, t;
-    __device__ Tiles(const MxGemm& g_, const int* cum_) : g(g_), cum(cum_), NB((g_.N + TM - 1) / TM), t(blockIdx.x) {
-        total = NB * (g.offsets ? cum[g.E] : (g.R + g.nt - 1) / g.nt);
+    int NB, KS, total, t;
+    long long u, end;  // split: the CTA's run of steps
+    __device__ Tiles(const MxGemm& g_, const int* cum_, int KS_)
+        : g(g_), cum(cum_), NB((g_.N + TM - 1) / TM), KS(KS_), t(blockIdx.x), u(-1), end(0) {
+        total = NB * (g.offsets ? cum[g.E] : (g.R + g.plan.nt - 1) / g.plan.nt);
+        const int ctas = gridDim.x;
+        // Runs of whole tiles lose up to a tile's time in the last round; past eight rounds that is little.
+        if (g.plan.split && (2 * total <= ctas || (total > ctas && total < 8 * ctas && total % ctas))) {
+            const int parts = 2 * total <= ctas ? 2 * total : ctas;
+            const long long steps = (long long)total * KS, c = blockIdx.x;
+            u = c < parts ? c * steps / parts : 0;
+            end = c < parts ? (c + 1) * steps / parts : 0;
+        }
     }
     __device__ bool next(Tile& o) {
-        if (t >= total) return false;
+        int tile = t;
+        o.k0 = 0;
+        o.k1 = KS;
+        if (u >= 0) {
+            if (u >= end) return false;
+            tile = (int)(u / KS);
+            o.k0 = (int)(u - (long long)tile * KS);
+            o.k1 = (int)min((long long)KS, o.k0 + (end - u));
+            u += o.k1 - o.k0;
+        } else {
+            if (t >= total) return false;
+            t += gridDim.x;
+        }
         int e = 0, i, first = 0, count = g.R;
         if (g.offsets) {
-            int hi = g.E;  // the largest e with cum[e] * NB <= t
+            int hi = g.E;  // the largest e with cum[e] * NB <= tile
             while (hi - e > 1) {
                 const int m = (e + hi) >> 1;
-                if (cum[m] * NB <= t) e = m;
+                if (cum[m] * NB <= tile) e = m;
                 else hi = m;
             }
-            const int nb = cum[e + 1] - cum[e], local = t - cum[e] * NB;
+            const int nb = cum[e + 1] - cum[e], local = tile - cum[e] * NB;
             o.wb = local / nb;
             i = local - o.wb * nb;
-            int end;
-            mx_segment(g.offsets, e, g.R, first, end);
-            count = end - first;
+            int last;
+            mx_segment(g.offsets, e, g.R, first, last);
+            count = last - first;
         } else {
-            const int nb = (g.R + g.nt - 1) / g.nt;
-            o.wb = t / nb;
-            i = t - o.wb * nb;
+            const int nb = (g.R + g.plan.nt - 1) / g.plan.nt;
+            o.wb = tile / nb;
+            i = tile - o.wb * nb;
         }
         o.expert = e;
-        o.row0 = first + i * g.nt;
-        o.rows = min(g.nt, count - i * g.nt);
-        o.slot = first / g.nt + e + i;
-        t += gridDim.x;
+        o.row0 = first + i * g.plan.nt;
+        o.rows = min(g.plan.nt, count - i * g.plan.nt);
+        o.slot = first / g.plan.nt + e + i;
         return true;
     }
 };
 
-template <bool A16>
+template <int MODE>
 __global__ void __launch_bounds__(kThreads, 1) k_mx_gemm(const __grid_constant__ MxParams p) {
     extern __shared__ uint8_t smem_raw[];
     __shared__ __align__(8) uint64_t bars[NBARS];
     __shared__ uint32_t tmem_slot;
     __shared__ int cum[1025];
-    constexpr int P = A16 ? 2 : 1;      // operand rows per token
-    constexpr int KBS = A16 ? 1 : 2;    // 128-column blocks per step
+    constexpr bool PARTS = MODE == kMxParts;
+    constexpr int KBS = PARTS ? 1 : 2;  // 128-column blocks per step
     const MxGemm& g = p.g;
     const uint32_t base = (smem_u32(smem_raw) + 1023u) & ~1023u;
     auto bar = [&](int i) { return smem_u32(&bars[i]); };
     const int warp = uniform(threadIdx.x >> 5), lane = threadIdx.x & 31;
     const int G = g.K / 128, KS = (G + KBS - 1) / KBS;
-    const int nblk = g.nblk;
+    const int nblk = g.plan.nblk;
     // A slot: weight codes, activation codes, weight scales (KBS blocks), activation scales (KBS x nblk blocks).
     const int b_off = A_BYTES, sa_off = p.stage_bytes - KBS * (1 + nblk) * 512, sb_off = sa_off + KBS * 512;
 
@@ -199,7 +239,7 @@ __global__ void __launch_bounds__(kThreads, 1) k_mx_gemm(const __grid_constant__
         for (int e = threadIdx.x; e < g.E; e += kThreads) {
             int a, b;
             if (!mx_segment(g.offsets, e, g.R, a, b)) atomicOr(g.err, (unsigned)QL_DEVERR_BOUNDS);
-            cum[e] = (b - a + g.nt - 1) / g.nt;
+            cum[e] = (b - a + g.plan.nt - 1) / g.plan.nt;
         }
         __syncthreads();
         if (warp == 3) {
@@ -224,7 +264,7 @@ __global__ void __launch_bounds__(kThreads, 1) k_mx_gemm(const __grid_constant__
     const uint32_t tmem = (uint32_t)uniform((int)tmem_slot);
     const unsigned long long lim = wait_limit(g.err);
     bool dead = false;
-    Tiles tiles(g, cum);
+    Tiles tiles(g, cum, KS);
     Tile ti;
 
     // The three issuing roles run as whole warps, with every operand the same in all lanes, and one elected lane
@@ -239,7 +279,7 @@ __global__ void __launch_bounds__(kThreads, 1) k_mx_gemm(const __grid_constant__
             const int expert = uniform(ti.expert), wb = uniform(ti.wb);
             const int row = expert * g.N + wb * TM;
             const uint8_t* sf = g.scales + ((long long)expert * NB + wb) * G * 512;
-            for (int k = 0; k < KS; ++k, ++step) {
+            for (int k = uniform(ti.k0), k1 = uniform(ti.k1); k < k1; ++k, ++step) {
                 if (!__all_sync(kFull, mbar_wait(bar(B_EMPTY + s), ph, lim))) {
                     dead = true;
                     break;
@@ -247,7 +287,7 @@ __global__ void __launch_bounds__(kThreads, 1) k_mx_gemm(const __grid_constant__
                 const unsigned sfb = min(KBS, G - k * KBS) * 512;
                 const uint32_t slot = base + s * p.stage_bytes, fb = bar(B_FULL + s);
                 if (leader) {
-                    mbar_expect_tx(fb, (A16 ? A_BYTES / 2 : A_BYTES) + sfb);  // spread copies count the packed bytes
+                    mbar_expect_tx(fb, (PARTS ? A_BYTES / 2 : A_BYTES) + sfb);  // spread copies count the packed bytes
                     tma_load_2d(slot, &p.tmW, k * 128, row, fb);
                     bulk_load(slot + sa_off, sf + (long long)k * KBS * 512, sfb, fb);
                 }
@@ -267,9 +307,10 @@ __global__ void __launch_bounds__(kThreads, 1) k_mx_gemm(const __grid_constant__
         asm volatile("griddepcontrol.wait;\n" ::: "memory");  // the quantiser's codes and scales
         int step = 0, s = 0, ph = 1;
         while (!dead && tiles.next(ti)) {
-            const int n16 = uniform(mx_pad16(ti.rows)), row0 = uniform(ti.row0);
+            const int cols = uniform(columns<MODE>(ti.rows)), row0 = uniform(ti.row0);
+            const int n = PARTS ? cols / 2 : cols;  // rows to bring, of each part
             const uint8_t* sf = g.xs + (long long)uniform(ti.slot) * G * nblk * 512;
-            for (int k = 0; k < KS; ++k, ++step) {
+            for (int k = uniform(ti.k0), k1 = uniform(ti.k1); k < k1; ++k, ++step) {
                 if (!__all_sync(kFull, mbar_wait(bar(B_EMPTY + s), ph, lim))) {
                     dead = true;
                     break;
@@ -277,13 +318,14 @@ __global__ void __launch_bounds__(kThreads, 1) k_mx_gemm(const __grid_constant__
                 const unsigned sfb = min(KBS, G - k * KBS) * nblk * 512;
                 const uint32_t slot = base + s * p.stage_bytes, fb = bar(B_FULL + s);
                 if (leader) {
-                    mbar_expect_tx(fb, P * n16 * 128 + sfb);
-                    for (int pl = 0; pl < P; ++pl) {
-                        const int row = pl * g.R + row0;
-                        const uint32_t dst = slot + b_off + pl * n16 * 128;
+                    mbar_expect_tx(fb, cols * 128 + sfb);
+#pragma unroll
+                    for (int pl = 0; pl < (PARTS ? 2 : 1); ++pl) {
+                        const int row = MODE == kMxDigits ? 8 * row0 : pl * g.R + row0;
+                        const uint32_t dst = slot + b_off + pl * n * 128;
                         int r = 0;
-                        for (; r + BIG <= n16; r += BIG) tma_load_2d(dst + r * 128, &p.tmXb, k * 128, row + r, fb);
-                        for (; r < n16; r += SMALL) tma_load_2d(dst + r * 128, &p.tmX, k * 128, row + r, fb);
+                        for (; r + BIG <= n; r += BIG) tma_load_2d(dst + r * 128, &p.tmXb, k * 128, row + r, fb);
+                        for (; r < n; r += SMALL) tma_load_2d(dst + r * 128, &p.tmX, k * 128, row + r, fb);
                     }
                     bulk_load(slot + sb_off, sf + (long long)k * KBS * nblk * 512, sfb, fb);
                 }
@@ -301,8 +343,9 @@ __global__ void __launch_bounds__(kThreads, 1) k_mx_gemm(const __grid_constant__
                 dead = true;
                 break;
             }
-            const uint32_t d = tmem + b * p.acc_cols, id0 = idesc<A16>(P * uniform(mx_pad16(ti.rows)));
-            for (int k = 0; k < KS; ++k) {
+            const uint32_t d = tmem + b * p.acc_cols, id0 = idesc<MODE>(uniform(columns<MODE>(ti.rows)));
+            const int k0 = uniform(ti.k0), k1 = uniform(ti.k1);
+            for (int k = k0; k < k1; ++k) {
                 if (!__all_sync(kFull, mbar_wait(bar(B_FULL + s), ph, lim))) {
                     dead = true;
                     break;
@@ -324,10 +367,10 @@ __global__ void __launch_bounds__(kThreads, 1) k_mx_gemm(const __grid_constant__
                     }
 #pragma unroll
                     for (int j = 0; j < 4; ++j) {  // 32 bytes of every row: +2 in the descriptors' address field
-                        const int q = A16 ? 0 : j >> 1, byte = A16 ? j : 2 * (j & 1);  // its scales' block and byte
+                        const int q = PARTS ? 0 : j >> 1, byte = PARTS ? j : 2 * (j & 1);  // its scales' block and byte
                         if (q < kbs)
-                            mma<A16>(d, ad + 2 * j, bd + 2 * j, id0 | (uint32_t)byte << 4 | (uint32_t)byte << 29,
-                                     sf + 4 * q, sfb + 4 * nblk * q, (k | j) ? 1u : 0u);
+                            mma<MODE>(d, ad + 2 * j, bd + 2 * j, id0 | (uint32_t)byte << 4 | (uint32_t)byte << 29,
+                                     sf + 4 * q, sfb + 4 * nblk * q, (k > k0 || j) ? 1u : 0u);
                     }
                     commit(bar(B_EMPTY + s));  // the slot and its scale columns may be refilled once these are done
                 }
@@ -343,9 +386,10 @@ __global__ void __launch_bounds__(kThreads, 1) k_mx_gemm(const __grid_constant__
         __all_sync(kFull, mbar_wait(bar(B_DRAIN), 0));
     } else if (warp >= kEpiWarp0) {  // ---- epilogue ----
         const int q = warp & 3;
+        asm volatile("griddepcontrol.wait;\n" ::: "memory");  // the quantiser's factors and zeroed outputs
         int tl = 0;
         while (tiles.next(ti)) {
-            const int b = tl & 1, n16 = mx_pad16(ti.rows);
+            const int b = tl & 1;
             const int n = ti.wb * TM + 32 * q + lane;
             const uint32_t d = tmem + b * p.acc_cols + ((uint32_t)(32 * q) << 16);
             if (!__all_sync(kFull, mbar_wait(bar(B_ACCF + b), (tl >> 1) & 1, lim))) {  // together
@@ -353,22 +397,50 @@ __global__ void __launch_bounds__(kThreads, 1) k_mx_gemm(const __grid_constant__
                 break;
             }
             fence_after();
-            for (int c0 = 0; c0 < ti.rows; c0 += CW) {
+            const bool part = ti.k1 - ti.k0 < KS, mine = n < g.N;
+            constexpr int TW = MODE == kMxDigits ? CW / 8 : CW;  // tokens of a read
+            for (int c0 = 0; c0 < ti.rows; c0 += TW) {
                 uint32_t v[CW], lo[CW];
-                tmem_ld16(d + c0, v);
-                if constexpr (A16) tmem_ld16(d + n16 + c0, lo);
-                tmem_wait_ld();
-#pragma unroll
-                for (int i = 0; i < CW; ++i) {
-                    if (c0 + i >= ti.rows) break;
-                    long long row = ti.row0 + c0 + i;
+                tmem_ld16(d + (MODE == kMxDigits ? 8 : 1) * c0, v);
+                if constexpr (PARTS) tmem_ld16(d + mx_pad16(ti.rows) + c0, lo);
+                // Lane i: the output row of the read's token i, -1 past the block.
+                int to = -1;
+                float factor = 1.0f;
+                if (lane < TW && c0 + lane < ti.rows) {
+                    to = ti.row0 + c0 + lane;
+                    if constexpr (MODE == kMxDigits) factor = g.xf[to];
                     if (g.perm) {
-                        row = __ldg(g.perm + row);
-                        if (row < 0 || row >= g.R) continue;
+                        to = __ldg(g.perm + to);
+                        if (to >= g.R) to = -1;
                     }
-                    float f = __uint_as_float(v[i]);
-                    if constexpr (A16) f += __uint_as_float(lo[i]);
-                    if (n < g.N) g.y[row * g.N + n] = f;
+                }
+                tmem_wait_ld();
+                float f[TW];
+#pragma unroll
+                for (int i = 0; i < TW; ++i) {
+                    if constexpr (MODE == kMxDigits) {  // small digits first
+                        const float* w = reinterpret_cast<const float*>(v + 8 * i);
+                        f[i] = ((w[0] + w[1]) + ((w[2] + w[3]) + ((w[4] + w[5]) + (w[6] + w[7])))) *
+                               __shfl_sync(kFull, factor, i);
+                    } else {
+                        f[i] = __uint_as_float(v[i]);
+                        if constexpr (PARTS) f[i] += __uint_as_float(lo[i]);
+                    }
+                }
+                if (!g.perm && !part && c0 + TW <= ti.rows) {  // the common case: rows one after another
+                    float* y = g.y + (long long)(ti.row0 + c0) * g.N + n;
+#pragma unroll
+                    for (int i = 0; i < TW; ++i, y += g.N)
+                        if (mine) *y = f[i];
+                } else {
+#pragma unroll
+                    for (int i = 0; i < TW; ++i) {
+                        const int row = __shfl_sync(kFull, to, i);
+                        float* const y = g.y + (long long)row * g.N + n;
+                        if (row < 0 || !mine) continue;
+                        if (part) atomicAdd(y, f[i]);
+                        else *y = f[i];
+                    }
                 }
             }
             fence_before();
@@ -387,28 +459,29 @@ __global__ void __launch_bounds__(kThreads, 1) k_mx_gemm(const __grid_constant__
     }
 }
 
-template <bool A16>
+template <int MODE>
 cudaError_t run(const MxGemm& g, cudaStream_t s) {
     DeviceInfo di;
     cudaError_t e = device_info(&di);
     if (e != cudaSuccess) return e;
-    constexpr int P = A16 ? 2 : 1, KBS = A16 ? 1 : 2;
+    constexpr bool PARTS = MODE == kMxParts;
+    constexpr int P = mx_planes(MODE), KBS = PARTS ? 1 : 2;
     MxParams p;
     p.g = g;
-    const int rows = P * g.nt;  // operand rows of a full token block
-    p.stage_bytes = (int)align_up(A_BYTES + rows * 128 + KBS * (1 + g.nblk) * 512, 1024);
+    const int nblk = g.plan.nblk, rows = P * g.plan.nt;  // operand rows of a full token block
+    p.stage_bytes = (int)align_up(A_BYTES + rows * 128 + KBS * (1 + nblk) * 512, 1024);
     p.acc_cols = (int)align_up(rows, 32);
     p.sf0 = 2 * p.acc_cols;
-    p.sf_cols = KBS * 4 * (1 + g.nblk);
+    p.sf_cols = KBS * 4 * (1 + nblk);
     const int smem_max = (int)(di.smem_optin < (size_t)kSmemMax ? di.smem_optin : kSmemMax) - 8 * 1024;
     p.stages = (smem_max - 1024) / p.stage_bytes;
     if (p.stages > ((int)kTmemCols - p.sf0) / p.sf_cols) p.stages = ((int)kTmemCols - p.sf0) / p.sf_cols;
     if (p.stages > kMaxStages) p.stages = kMaxStages;
     if (p.stages < 2) return cudaErrorInvalidValue;
     const int smem = p.stages * p.stage_bytes + 1024;
-    const long long wrows = (long long)g.E * g.N, xrows = (long long)P * g.R, xbytes = A16 ? g.K : g.K / 2;
-    e = A16 ? make_tmap_u4_spread(g.codes, wrows, g.K, TM, &p.tmW)
-            : make_tmap_2d(g.codes, wrows, g.K / 2, g.K / 2, 128, TM, CU_TENSOR_MAP_SWIZZLE_128B, &p.tmW);
+    const long long wrows = (long long)g.E * g.N, xrows = (long long)P * g.R, xbytes = PARTS ? g.K : g.K / 2;
+    e = PARTS ? make_tmap_u4_spread(g.codes, wrows, g.K, TM, &p.tmW)
+              : make_tmap_2d(g.codes, wrows, g.K / 2, g.K / 2, 128, TM, CU_TENSOR_MAP_SWIZZLE_128B, &p.tmW);
     if (e == cudaSuccess) e = make_tmap_2d(g.xq, xrows, xbytes, xbytes, 128, SMALL, CU_TENSOR_MAP_SWIZZLE_128B, &p.tmX);
     if (e == cudaSuccess) e = make_tmap_2d(g.xq, xrows, xbytes, xbytes, 128, BIG, CU_TENSOR_MAP_SWIZZLE_128B, &p.tmXb);
     if (e != cudaSuccess) return e;
@@ -417,13 +490,14 @@ cudaError_t run(const MxGemm& g, cudaStream_t s) {
     int dev = 0;
     cudaGetDevice(&dev);
     if (dev >= 64 || !attr_set[dev]) {
-        e = cudaFuncSetAttribute(k_mx_gemm<A16>, cudaFuncAttributeMaxDynamicSharedMemorySize, kSmemMax - 8 * 1024);
+        e = cudaFuncSetAttribute(k_mx_gemm<MODE>, cudaFuncAttributeMaxDynamicSharedMemorySize, kSmemMax - 8 * 1024);
         if (e != cudaSuccess) return e;
         if (dev < 64) attr_set[dev] = true;
     }
-    const long long tiles = (long long)((g.N + TM - 1) / TM) * mx_slots(g.R, g.offsets ? g.E : 0, g.nt);
+    const long long tiles = (long long)((g.N + TM - 1) / TM) * mx_slots(g.R, g.offsets ? g.E : 0, g.plan.nt);
+    const long long ctas = (g.plan.split ? 2 : 1) * tiles;
     cudaLaunchConfig_t cfg = {};
-    cfg.gridDim = dim3((unsigned)(tiles < di.sm_count ? tiles : di.sm_count));
+    cfg.gridDim = dim3((unsigned)(ctas < di.sm_count ? ctas : di.sm_count));
     cfg.blockDim = dim3(kThreads);
     cfg.dynamicSmemBytes = smem;
     cfg.stream = s;
@@ -432,25 +506,37 @@ cudaError_t run(const MxGemm& g, cudaStream_t s) {
     attr[0].val.programmaticStreamSerializationAllowed = 1;  // after this library's quantiser
     cfg.attrs = attr;
     cfg.numAttrs = 1;
-    e = cudaLaunchKernelEx(&cfg, k_mx_gemm<A16>, p);
+    e = cudaLaunchKernelEx(&cfg, k_mx_gemm<MODE>, p);
     return e != cudaSuccess ? e : cudaGetLastError();
 }
 
 }  // namespace
 
-// Rows of a token block: the widest the accumulators allow, cut evenly over one weight's rows; for experts
-// twice the average count, so that most experts are one block (a block costs its own rows alone, but a second
-// one reads the weights again).
-int mx_tokens(bool a16, int R, int E) {
-    const int most = a16 ? kMxTokens / 2 : kMxTokens;
-    if (!E) {
-        const int blocks = (int)(((long long)R + most - 1) / most);
-        return mx_pad16((int)(((long long)R + blocks - 1) / blocks));
-    }
-    const long long avg2 = (2LL * R + E - 1) / E;
-    return avg2 >= most ? most : mx_pad16((int)avg2);
+// Tokens of a block: the widest the accumulators allow, cut evenly over one weight's rows; for experts twice the
+// average count, so that most experts are one block (a block costs its own rows alone, but a second one reads
+// the weights again).
+MxPlan mx_plan(bool a16, int R, int N, int K, int E, int sms) {
+    (void)K;
+    MxPlan p;
+    const long long per = E ? (R + E - 1) / E : R;  // rows an expert
+    p.mode = !a16 ? kMxA4 : per <= (E ? 16 : 24) ? kMxDigits : kMxParts;
+    const int P = mx_planes(p.mode), most = kMxRows / P, step = p.mode == kMxDigits ? 2 : 16;
+    long long nt = E ? 2 * per : (R + (R + most - 1LL) / most - 1) / ((R + most - 1LL) / most);
+    if (nt > most) nt = most;
+    p.nt = (int)((nt + step - 1) / step * step);
+    p.nblk = (P * p.nt + 127) / 128;
+    // Cutting tiles along K costs a zeroed y: worth it while y is small beside the weights.
+    const long long tiles = (long long)((N + TM - 1) / TM) * mx_slots(R, 0, p.nt);
+    p.split = (long long)R * N * 4 <= (4 << 20) && (E || tiles < 8LL * sms);
+    return p;
 }
 
-cudaError_t launch_mx_gemm(const MxGemm& g, bool a16, cudaStream_t s) { return a16 ? run<true>(g, s) : run<false>(g, s); }
+cudaError_t launch_mx_gemm(const MxGemm& g, cudaStream_t s) {
+    switch (g.plan.mode) {
+    case kMxA4: return run<kMxA4>(g, s);
+    case kMxDigits: return run<kMxDigits>(g, s);
+    default: return run<kMxParts>(g, s);
+    }
+}
 
 }  // namespace ql

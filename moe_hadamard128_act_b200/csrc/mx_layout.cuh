@@ -11,12 +11,16 @@
 // cut, expert by expert, into token blocks of at most nt rows; block i of
 // expert e gets the slot number offsets[e] / nt + e + i, which no other block
 // has (an expert of c rows starts at most c / nt + 1 slots before the next), so
-// nothing has to be counted beforehand.  A slot's operand rows are its rows in
-// order, and for 16-bit activations the low parts of the same rows after them,
-// starting at the block's row count rounded up to 16.
+// nothing has to be counted beforehand.  A token is one or more operand rows of
+// its block (MxMode):
+//   kMxA4      its MXFP4 codes: row c.
+//   kMxDigits  16-bit activations as eight E2M1 digits: rows 8 c .. 8 c + 7.
+//   kMxParts   16-bit activations as two E4M3 parts: row c, and the low part's
+//              row n + c, n the block's tokens rounded up to 16.
 #pragma once
 
 #include "ql_device.cuh"
+#include "ql_internal.h"
 
 namespace ql {
 
@@ -25,12 +29,8 @@ __host__ __device__ __forceinline__ long long mx_scale_at(long long slot, int G,
     return ((slot * G + kb) * nblk + (r >> 7)) * 512 + (r & 31) * 16 + ((r >> 5) & 3) * 4;
 }
 
-__host__ __device__ __forceinline__ int mx_pad16(int rows) { return (rows + 15) & ~15; }
 
-// One token block: rows [row0, row0 + rows) of the sorted order.
-struct MxBlock {
-    int expert, row0, rows;  // rows = 0: an empty slot
-};
+__host__ __device__ __forceinline__ int mx_pad16(int rows) { return (rows + 15) & ~15; }
 
 // Segment of expert e in the sorted rows; empty when its offsets are out of order or out of [0, R].
 __device__ __forceinline__ bool mx_segment(const int32_t* offsets, int e, int R, int& a, int& b) {
@@ -72,56 +72,123 @@ __device__ __forceinline__ float mx_scale(uint32_t b) {
     return __uint_as_float(b == 0 ? 0x00400000u : b == 255 ? 0x7FFFFFFFu : b << 23);
 }
 
-// Largest magnitude of a 32-block held 4 values per lane by 8 neighbouring lanes, as fp32 bits without the
-// sign: unsigned order puts infinities and NaN above every finite value.
-__device__ __forceinline__ uint32_t mx_block_amax(const float v[4]) {
+// ---- 128 columns of a row held 8 neighbouring values a lane by 16 lanes (half a warp) -------------------
+// The Walsh-Hadamard transform of fwht128_warp, bit for bit: the same butterflies in the same order, strides
+// 1, 2, 4 inside the lane and 8 .. 64 across lanes.
+__device__ __forceinline__ void mx_fwht128(float v[8], int lane) {
+#pragma unroll
+    for (int s = 1; s < 8; s <<= 1)
+#pragma unroll
+        for (int i = 0; i < 8; ++i)
+            if (!(i & s)) {
+                const float a = v[i], b = v[i | s];
+                v[i] = __fadd_rn(a, b);
+                v[i | s] = __fsub_rn(a, b);
+            }
+#pragma unroll
+    for (int m = 1; m < 16; m <<= 1) {
+        const float sgn = (lane & m) ? -1.0f : 1.0f;
+#pragma unroll
+        for (int i = 0; i < 8; ++i) {
+            const float o = __shfl_xor_sync(kFull, v[i], m);
+            v[i] = __fmaf_rn(sgn, v[i], o);
+        }
+    }
+    const float c = fwht_scale();
+#pragma unroll
+    for (int i = 0; i < 8; ++i) v[i] = __fmul_rn(v[i], c);
+}
+
+// A 32-block's largest magnitude (4 lanes) as fp32 bits without the sign: unsigned order puts infinities and
+// NaN (exponent field 255) above every finite value.
+__device__ __forceinline__ uint32_t mx_block_max(const float v[8]) {
     uint32_t m = 0;
 #pragma unroll
-    for (int i = 0; i < 4; ++i) m = max(m, __float_as_uint(v[i]) & 0x7FFFFFFFu);
-#pragma unroll
-    for (int d = 1; d < 8; d <<= 1) m = max(m, __shfl_xor_sync(kFull, m, d));
-    return m;
+    for (int i = 0; i < 8; ++i) m = max(m, __float_as_uint(v[i]) & 0x7FFFFFFFu);
+    m = max(m, __shfl_xor_sync(kFull, m, 1));
+    return max(m, __shfl_xor_sync(kFull, m, 2));
+}
+// The four blocks' scale bytes as one word, in every lane of the half warp.
+__device__ __forceinline__ uint32_t mx_scale_word(uint32_t byte, int lane) {
+    uint32_t w = byte << (8 * ((lane >> 2) & 3));
+    w |= __shfl_xor_sync(kFull, w, 4);
+    return w | __shfl_xor_sync(kFull, w, 8);
 }
 
-// MXFP4 of a 32-block (4 values per lane): the lane's four codes (low nibble first) and the scale byte.
-// floor(log2 amax) is the exponent field, so the byte e + 127 with e = floor(log2 amax) - 2 is the field
-// less 2, clamped at 0; the division by 2^e is an exact product.
-__device__ __forceinline__ uint32_t mx_quant4(const float v[4], uint32_t& byte) {
-    const uint32_t ex = mx_block_amax(v) >> 23;
-    if (ex == 255) {  // an infinity or a NaN
-        byte = 255;
-        return 0;
-    }
+// MXFP4 of a 32-block: the lane's eight codes (low nibble first) and the scale byte.  floor(log2 amax) is the
+// exponent field, so the byte e + 127 with e = floor(log2 amax) - 2 is the field less 2, clamped at 0; the
+// division by 2^e is an exact product.
+__device__ __forceinline__ uint32_t mx_quant8(const float v[8], uint32_t& byte) {
+    const uint32_t ex = mx_block_max(v) >> 23;
     byte = ex > 2 ? ex - 2 : 0;
     const float inv = __uint_as_float((254u - byte) << 23);
-    return cvt_e2m1x2(v[1] * inv, v[0] * inv) | cvt_e2m1x2(v[3] * inv, v[2] * inv) << 8;
+    uint32_t c = 0;
+#pragma unroll
+    for (int i = 0; i < 4; ++i) c |= cvt_e2m1x2(v[2 * i + 1] * inv, v[2 * i] * inv) << (8 * i);
+    if (ex == 255) {  // an infinity or a NaN
+        byte = 255;
+        c = 0;
+    }
+    return c;
 }
 
-// A 32-block of bf16 values as two E4M3 parts (4 values per lane, low byte first), v = 2^e (hi + lo / 32):
-// e puts the block's largest magnitude into [128, 256), hi is v / 2^e rounded to E4M3's four significant
-// bits, and what is left of bf16's eight fits four more, so the sum is exact unless the value is so far below
-// the largest that lo's spacing 2^-9 cuts it: exact from 2^-14 of the largest up, within 2^-22 of it below.
-// byte: hi's scale; lo's is byte - 5 (e is held at -122 or more for that).
-__device__ __forceinline__ void mx_split4(const float v[4], uint32_t& hi, uint32_t& lo, uint32_t& byte) {
-    const uint32_t ex = mx_block_amax(v) >> 23;
-    hi = lo = 0;
-    if (ex == 255) {
-        byte = 255;
-        return;
+// A 32-block of bf16 values as eight E2M1 digits, v = 2^e sum_p d_p 8^-p: e puts the block's largest magnitude
+// into [2, 4), each digit is what is left rounded to E2M1 (off by at most 0.5 below 4), and eight times the
+// remainder, at most 4 again, goes to the next.  Every step is exact in fp32; after the eighth at most
+// 0.5 * 8^-7 of 2^e is left, 2^-23 of the largest magnitude, and nothing of values down to 2^-16 of it.
+// byte: the first digit's scale; digit p's is byte - 3 p, so it is held at 21 or more: a block below 2^-105
+// loses its last digits, unless its whole row is small and was scaled up by 2^up (see k_mx_act).
+__device__ __forceinline__ void mx_digits8(const float v[8], uint32_t ex, int up, uint32_t d[8], uint32_t& byte) {
+    byte = (uint32_t)max((int)ex - 1 + up, 21);
+    // 2^-e has the exponent field f; past 254 as a product of two powers (with up only).
+    const int f = 254 - ((int)byte - up);
+    const float i0 = __uint_as_float((uint32_t)min(f, 254) << 23), i1 = __uint_as_float((uint32_t)(127 + max(f - 254, 0)) << 23);
+    float r[8];
+#pragma unroll
+    for (int i = 0; i < 8; ++i) r[i] = v[i] * i0 * i1;
+#pragma unroll
+    for (int p = 0; p < 8; ++p) {
+        d[p] = 0;
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+            const uint32_t c = cvt_e2m1x2(r[2 * i + 1], r[2 * i]);
+            d[p] |= c << (8 * i);
+            const uint32_t h = e2m1x2_to_f16x2(c);
+            r[2 * i] = (r[2 * i] - f16_bits_to_float((uint16_t)h)) * 8.0f;
+            r[2 * i + 1] = (r[2 * i + 1] - f16_bits_to_float((uint16_t)(h >> 16))) * 8.0f;
+        }
     }
+    if (ex == 255) {  // an infinity or a NaN
+        byte = 255;
+#pragma unroll
+        for (int p = 0; p < 8; ++p) d[p] = 0;
+    }
+}
+
+// A 32-block of bf16 values as two E4M3 parts (low byte first), v = 2^e (hi + lo / 32): e puts the block's
+// largest magnitude into [128, 256), hi is v / 2^e rounded to E4M3's four significant bits, and what is left of
+// bf16's eight fits four more, so the sum is exact unless the value is so far below the largest that lo's
+// spacing 2^-9 cuts it: exact from 2^-14 of the largest up, within 2^-22 of it below.  byte: hi's scale; lo's
+// is byte - 5 (e is held at -122 or more for that), or 255 with it.
+__device__ __forceinline__ void mx_split8(const float v[8], uint2& hi, uint2& lo, uint32_t& byte) {
+    const uint32_t ex = mx_block_max(v) >> 23;
     byte = ex > 12 ? ex - 7 : 5;
     const float inv = __uint_as_float((254u - byte) << 23);
-    float s[4];
+    uint32_t h[4], l[4];
 #pragma unroll
-    for (int i = 0; i < 4; ++i) s[i] = v[i] * inv;
-    hi = cvt_e4m3x2(s[1], s[0]) | cvt_e4m3x2(s[3], s[2]) << 16;
-#pragma unroll
-    for (int i = 0; i < 2; ++i) {
-        const uint32_t h = e4m3x2_to_f16x2(hi >> (16 * i));
-        s[2 * i] -= f16_bits_to_float((uint16_t)h);
-        s[2 * i + 1] -= f16_bits_to_float((uint16_t)(h >> 16));
+    for (int i = 0; i < 4; ++i) {
+        const float a = v[2 * i] * inv, b = v[2 * i + 1] * inv;
+        h[i] = cvt_e4m3x2(b, a);
+        const uint32_t f = e4m3x2_to_f16x2(h[i]);
+        l[i] = cvt_e4m3x2((b - f16_bits_to_float((uint16_t)(f >> 16))) * 32.0f,
+                          (a - f16_bits_to_float((uint16_t)f)) * 32.0f);
     }
-    lo = cvt_e4m3x2(s[1] * 32.0f, s[0] * 32.0f) | cvt_e4m3x2(s[3] * 32.0f, s[2] * 32.0f) << 16;
+    hi = make_uint2(h[0] | h[1] << 16, h[2] | h[3] << 16);
+    lo = make_uint2(l[0] | l[1] << 16, l[2] | l[3] << 16);
+    if (ex == 255) {  // an infinity or a NaN
+        byte = 255;
+        hi = lo = make_uint2(0, 0);
+    }
 }
 
 }  // namespace ql

@@ -164,42 +164,44 @@ FwdWs forward_ws(int fmt, size_t M, size_t N, size_t K) {
 // The MXFP4 product over R rows: quantised activations, their scales in the order of the product's tiles,
 // and, for pairs given by routing ids, their permutation.
 struct MxWs {
-    int nt, nblk;
-    size_t xq, xs, counts, offsets, perm, total;
+    MxPlan plan;
+    size_t xq, xs, xf, counts, offsets, perm, inv, total;
 };
-MxWs mx_ws(int fmt, long long R, long long K, int E, bool pairs) {
-    const bool a16 = fmt == QL_MXFP4_G32;
+MxWs mx_ws(int fmt, int R, int N, int K, int E, bool pairs) {
+    DeviceInfo di;
     MxWs w;
-    w.nt = mx_tokens(a16, (int)R, E);
-    w.nblk = mx_nblk(a16, w.nt);
+    w.plan = mx_plan(fmt == QL_MXFP4_G32, R, N, K, E, device_info(&di) == cudaSuccess ? di.sm_count : 148);
+    const size_t row = w.plan.mode == kMxA4 ? K / 2 : w.plan.mode == kMxDigits ? (size_t)4 * K : (size_t)2 * K;
     size_t o = 0;
-    w.xq = o; o += align_up((size_t)R * (a16 ? 2 * K : K / 2), 256);
-    w.xs = o; o += align_up((size_t)mx_slots((int)R, E, w.nt) * (K / 128) * w.nblk * 512, 256);
-    w.counts = w.offsets = w.perm = 0;
+    w.xq = o; o += align_up((size_t)R * row, 256);
+    w.xs = o; o += align_up((size_t)mx_slots(R, E, w.plan.nt) * (K / 128) * w.plan.nblk * 512, 256);
+    w.xf = o; o += w.plan.mode == kMxDigits ? align_up((size_t)R * 4, 256) : 0;
+    w.counts = w.offsets = w.perm = w.inv = 0;
     if (pairs) {
         w.counts = o; o += align_up((size_t)E * 4, 256);
         w.offsets = o; o += align_up(((size_t)E + 1) * 4, 256);
         w.perm = o; o += align_up((size_t)R * 4, 256);
+        w.inv = o; o += align_up((size_t)R * 4, 256);
     }
     w.total = o;
     return w;
 }
 
 // Quantise the activations, then the product.  E = 0: one weight over every row.
-int mx_product(const void* x, const void* codes, const void* scales, int fmt, int flags, int R, int N, int K, int E,
-               const int32_t* offsets, const int32_t* perm, int topk, const MxWs& w, uint8_t* ws, float* y,
-               unsigned* err, cudaStream_t s) {
-    const bool a16 = fmt == QL_MXFP4_G32;
-    MxAct q{static_cast<const __nv_bfloat16*>(x), R, K, (flags & QL_HADAMARD) ? 1 : 0, w.nt, w.nblk, offsets, E, perm,
-            topk, ws + w.xq, ws + w.xs};
+int mx_product(const void* x, const void* codes, const void* scales, int flags, int R, int N, int K, int E,
+               const int32_t* offsets, const int32_t* perm, const int32_t* ids, int topk, const MxWs& w, uint8_t* ws,
+               float* y, unsigned* err, cudaStream_t s) {
+    MxAct q{static_cast<const __nv_bfloat16*>(x), R, K, (flags & QL_HADAMARD) ? 1 : 0, w.plan, offsets, E, ids,
+            ids ? reinterpret_cast<const int32_t*>(ws + w.inv) : nullptr, topk, ws + w.xq, ws + w.xs,
+            reinterpret_cast<float*>(ws + w.xf), y, N};
     int t = trace_begin(QL_KIND_ACT_QUANT, s);
-    cudaError_t e = launch_mx_act(q, a16, s);
+    cudaError_t e = launch_mx_act(q, s);
     trace_end(t, s);
     if (e != cudaSuccess) return from_cuda(e);
-    MxGemm g{static_cast<const uint8_t*>(codes), static_cast<const uint8_t*>(scales), q.codes, q.scales, offsets, perm,
-             y, err, R, E ? E : 1, N, K, w.nt, w.nblk};
+    MxGemm g{static_cast<const uint8_t*>(codes), static_cast<const uint8_t*>(scales), q.codes, q.scales, q.factors,
+             offsets, perm, y, err, R, E ? E : 1, N, K, w.plan};
     t = trace_begin(E ? QL_KIND_MOE_GEMM : QL_KIND_MX_GEMM, s);
-    e = launch_mx_gemm(g, a16, s);
+    e = launch_mx_gemm(g, s);
     trace_end(t, s);
     return from_cuda(e);
 }
@@ -399,7 +401,7 @@ int qlinear_workspace_size(int fmt, int flags, int M, int N, int K, size_t* byte
     if (!fmt_valid(fmt) || M < 1 || N < 1 || K < 128 || K % 128 || (flags & ~(QL_HADAMARD | QL_SCALE_SEARCH)) ||
         !bytes)
         return QL_EINVAL;
-    *bytes = fmt_mxfp4(fmt) ? mx_ws(fmt, M, K, 0, false).total : forward_ws(fmt, M, N, K).total();
+    *bytes = fmt_mxfp4(fmt) ? mx_ws(fmt, M, N, K, 0, false).total : forward_ws(fmt, M, N, K).total();
     return QL_OK;
 }
 
@@ -415,13 +417,13 @@ int qlinear_forward(const void* x, const void* W_packed, const void* scales, con
         (zeros && !aligned16(zeros)))
         return QL_EALIGN;
     if (fmt_mxfp4(fmt)) {
-        const MxWs w = mx_ws(fmt, M, K, 0, false);
+        const MxWs w = mx_ws(fmt, M, N, K, 0, false);
         if (!ws || ws_bytes < w.total) return QL_EWORKSPACE;
         if (!aligned16(ws)) return QL_EALIGN;
         DeviceInfo di;
         const cudaError_t e = device_info(&di);
         if (e != cudaSuccess) return from_cuda(e);
-        return mx_product(x, W_packed, scales, fmt, flags, M, N, K, 0, nullptr, nullptr, 1, w,
+        return mx_product(x, W_packed, scales, flags, M, N, K, 0, nullptr, nullptr, nullptr, 1, w,
                           static_cast<uint8_t*>(ws), y, di.err_word, static_cast<cudaStream_t>(stream));
     }
     const FwdWs w = forward_ws(fmt, M, N, K);
@@ -697,7 +699,7 @@ int moe_workspace_size(const ql_experts* experts, int T, int topk, size_t* bytes
     if (st != QL_OK) return st;
     if (T < 1 || topk < 1 || topk > 64 || !bytes) return QL_EINVAL;
     if (fmt_mxfp4(experts->fmt) && (long long)T * topk > INT32_MAX) return QL_EINVAL;
-    *bytes = fmt_mxfp4(experts->fmt) ? mx_ws(experts->fmt, (long long)T * topk, experts->K, experts->E, true).total
+    *bytes = fmt_mxfp4(experts->fmt) ? mx_ws(experts->fmt, T * topk, experts->N, experts->K, experts->E, true).total
                                      : moe_ws(experts, T, topk).total;
     return QL_OK;
 }
@@ -712,7 +714,7 @@ int moe_gate_up(const void* x, const int32_t* topk_ids, const float* topk_weight
     if (fmt_mxfp4(experts->fmt)) {
         if ((long long)T * topk > INT32_MAX) return QL_EINVAL;
         const int R = T * topk;
-        const MxWs w = mx_ws(experts->fmt, R, experts->K, experts->E, true);
+        const MxWs w = mx_ws(experts->fmt, R, experts->N, experts->K, experts->E, true);
         if (!ws || ws_bytes < w.total) return QL_EWORKSPACE;
         if (!aligned16(ws)) return QL_EALIGN;
         DeviceInfo di;
@@ -724,14 +726,15 @@ int moe_gate_up(const void* x, const int32_t* topk_ids, const float* topk_weight
         int32_t* const offsets = reinterpret_cast<int32_t*>(b + w.offsets);
         int32_t* const perm = reinterpret_cast<int32_t*>(b + w.perm);
         MoePermuteOut po;
+        po.inv = reinterpret_cast<int32_t*>(b + w.inv);
         po.yz = y;  // rows of pairs with a bad expert id are zeroed
         po.N = experts->N;
         const int t = trace_begin(QL_KIND_MOE_PERMUTE, s);
         e = launch_moe_permute(topk_ids, T, topk, experts->E, counts, offsets, perm, po, di.err_word, s);
         trace_end(t, s);
         if (e != cudaSuccess) return from_cuda(e);
-        return mx_product(x, experts->codes, experts->scales, experts->fmt, experts->flags, R, experts->N, experts->K,
-                          experts->E, offsets, perm, topk, w, b, y, di.err_word, s);
+        return mx_product(x, experts->codes, experts->scales, experts->flags, R, experts->N, experts->K,
+                          experts->E, offsets, perm, topk_ids, topk, w, b, y, di.err_word, s);
     }
     const MoeWs w = moe_ws(experts, T, topk);
     if (!ws || ws_bytes < w.total) return QL_EWORKSPACE;
@@ -835,7 +838,7 @@ int qlinear_grouped_workspace_size(const ql_experts* experts, int R, size_t* byt
     if (st != QL_OK) return st;
     if (!fmt_mxfp4(experts->fmt)) return QL_EUNSUPPORTED;
     if (R < 1 || !bytes) return QL_EINVAL;
-    *bytes = mx_ws(experts->fmt, R, experts->K, experts->E, false).total;
+    *bytes = mx_ws(experts->fmt, R, experts->N, experts->K, experts->E, false).total;
     return QL_OK;
 }
 
@@ -846,14 +849,14 @@ int qlinear_grouped(const void* x, const int32_t* offsets, const ql_experts* exp
     if (!fmt_mxfp4(experts->fmt)) return QL_EUNSUPPORTED;
     if (R < 1 || !x || !offsets || !y) return QL_EINVAL;
     if (!aligned16(x) || !aligned16(offsets) || !aligned16(y)) return QL_EALIGN;
-    const MxWs w = mx_ws(experts->fmt, R, experts->K, experts->E, false);
+    const MxWs w = mx_ws(experts->fmt, R, experts->N, experts->K, experts->E, false);
     if (!ws || ws_bytes < w.total) return QL_EWORKSPACE;
     if (!aligned16(ws)) return QL_EALIGN;
     DeviceInfo di;
     const cudaError_t e = device_info(&di);
     if (e != cudaSuccess) return from_cuda(e);
-    return mx_product(x, experts->codes, experts->scales, experts->fmt, experts->flags, R, experts->N, experts->K,
-                      experts->E, offsets, nullptr, 1, w, static_cast<uint8_t*>(ws), y, di.err_word,
+    return mx_product(x, experts->codes, experts->scales, experts->flags, R, experts->N, experts->K,
+                      experts->E, offsets, nullptr, nullptr, 1, w, static_cast<uint8_t*>(ws), y, di.err_word,
                       static_cast<cudaStream_t>(stream));
 }
 

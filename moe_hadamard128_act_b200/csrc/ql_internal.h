@@ -241,37 +241,50 @@ cudaError_t launch_mx_quant_rows(const void* x, int M, int K, int rotate, uint8_
 cudaError_t launch_mx_pack(const uint8_t* codes_in, const uint8_t* scales_in, int N, int K, uint8_t* codes,
                            uint8_t* scales, unsigned* err, cudaStream_t s);
 cudaError_t launch_mx_dequant(const uint8_t* codes, const uint8_t* scales, int N, int K, void* out, cudaStream_t s);
-// The product's activations: R rows, sorted by expert when offsets [E + 1] is given, from x row r or
-// perm[r] / topk; token blocks of at most nt rows, nblk scale blocks per 128 columns of a slot.
+// How the product takes x (see mx_layout.cuh): 4-bit, or 16-bit as eight 4-bit digits or as two 8-bit parts.
+enum MxMode { kMxA4 = 0, kMxDigits = 1, kMxParts = 2 };
+__host__ __device__ constexpr int mx_planes(int mode) { return mode == kMxA4 ? 1 : mode == kMxDigits ? 8 : 2; }
+constexpr int kMxRows = 192;   // operand rows of a token block at most
+constexpr int kMxTopk = 64;    // pairs of a token at most
+// What the host decides for a product over R rows: the mode, the tokens of a block at most, scale blocks per 128
+// columns of a slot, and whether tiles may be cut along K between two CTAs (y is then zeroed by the quantiser).
+struct MxPlan {
+    int mode, nt, nblk, split;
+};
+MxPlan mx_plan(bool a16, int R, int N, int K, int E, int sms);
+inline long long mx_slots(int R, int E, int nt) { return E ? (long long)R / nt + E + 1 : ((long long)R + nt - 1) / nt; }
+// The product's activations: R sorted rows.  Rows of x are sorted rows themselves (ids null; offsets [E + 1] null:
+// one expert owns all), or tokens whose topk pairs, of experts ids[t * topk + j], sit at sorted rows
+// inv[t * topk + j].
 struct MxAct {
     const __nv_bfloat16* x;
     int R, K, rotate;
-    int nt, nblk;
+    MxPlan plan;
     const int32_t* offsets;
     int E;
-    const int32_t* perm;
+    const int32_t *ids, *inv;
     int topk;
-    uint8_t* codes;   // E2M1 [R][K / 2], or E4M3 parts [2][R][K]
+    uint8_t* codes;   // E2M1 [R][K / 2], digits [8 R][K / 2], or E4M3 parts [2][R][K]
     uint8_t* scales;  // [slots][K / 128][nblk][512]
+    float* factors;   // digits: what each sorted row's sums are to be multiplied by
+    float* y;         // plan.split: the rows' outputs, zeroed here
+    int N;
 };
-cudaError_t launch_mx_act(const MxAct& a, bool a16, cudaStream_t s);
-constexpr int kMxTokens = 192;  // operand rows of a token block at most (16-bit activations: two per token)
-// Rows of a token block for this call, and the scale blocks and slots that follow from it.
-int mx_tokens(bool a16, int R, int E);
-inline int mx_nblk(bool a16, int nt) { return ((a16 ? 2 : 1) * nt + 127) / 128; }
-inline long long mx_slots(int R, int E, int nt) { return E ? (long long)R / nt + E + 1 : ((long long)R + nt - 1) / nt; }
+cudaError_t launch_mx_act(const MxAct& a, cudaStream_t s);
 struct MxGemm {
     const uint8_t* codes;   // [E][N][K / 2]
     const uint8_t* scales;  // [E][ceil(N / 128)][K / 128][512]
-    const uint8_t* xq;      // MxAct's codes and scales
+    const uint8_t* xq;      // MxAct's codes, scales and factors
     const uint8_t* xs;
+    const float* xf;
     const int32_t* offsets;  // null: one expert owns every row
     const int32_t* perm;     // row r goes to y row perm[r]; null: to row r
     float* y;                // [R][N]
     unsigned* err;
-    int R, E, N, K, nt, nblk;
+    int R, E, N, K;
+    MxPlan plan;
 };
-cudaError_t launch_mx_gemm(const MxGemm& a, bool a16, cudaStream_t s);
+cudaError_t launch_mx_gemm(const MxGemm& g, cudaStream_t s);
 
 // ---- launch trace (ql_trace_enable / ql_trace_read) --------------------------------------
 // trace_begin records a start event for one library launch when tracing is on
