@@ -65,9 +65,9 @@ __global__ void __launch_bounds__(kWarps * 32) k_mx_quant(const T* W, int N, int
 // null, or sorted rows given), or one for each of the token's topk pairs, at the pair's position inv[] in its
 // expert's segment.
 struct Place {
-    long long slot;
-    int row, c, low;  // sorted row (-1: none), token of its block, operand row of its low part
-    long long y;      // output row
+    uint8_t *codes, *scale, *low;  // where the row's codes, its scales and its low part's scales begin
+    float* y;                      // its output
+    int row, c;                    // sorted row (-1: none), token of its block
 };
 
 // Digits: 32, and a factor of 2^-32 on the row's sums, if no magnitude of the row (rotated and rounded as the
@@ -91,7 +91,10 @@ __device__ __noinline__ int row_up(const __nv_bfloat16* x, int G, int rotate) {
 
 template <int MODE>
 __global__ void __launch_bounds__(kWarps * 32) k_mx_act(const MxAct a) {
-    asm volatile("griddepcontrol.launch_dependents;\n" ::: "memory");  // let the product start its weight stream
+    // Launched while the kernel before it ends: nothing is read or written before that one is done, and only then
+    // may the product start its weight stream, which waits for nothing else.
+    asm volatile("griddepcontrol.wait;\n" ::: "memory");
+    asm volatile("griddepcontrol.launch_dependents;\n" ::: "memory");
     __shared__ Place places[kMxTopk];
     const int G = a.K / 128, x = blockIdx.x, nt = a.plan.nt, nblk = a.plan.nblk;
     const int dests = a.ids ? a.topk : 1;
@@ -111,15 +114,21 @@ __global__ void __launch_bounds__(kWarps * 32) k_mx_act(const MxAct a) {
             if (r < first || r >= end) r = -1;  // a row of no expert
         }
         const int i = r < 0 ? 0 : (r - first) / nt, c = r < 0 ? 0 : (r - first) - i * nt;
-        if ((threadIdx.x & 31) == 0)
-            places[j] = Place{first / nt + e + i, r, c, mx_pad16(min(nt, end - first - i * nt)) + c, y};
+        if ((threadIdx.x & 31) == 0) {
+            const long long slot = first / nt + e + i;
+            const int low = mx_pad16(min(nt, end - first - i * nt)) + c;
+            const long long at = MODE == kMxA4 ? (long long)r * (a.K / 2)
+                                               : MODE == kMxDigits ? 4LL * r * a.K : (long long)r * a.K;
+            places[j] = Place{a.codes + at, a.scales + mx_scale_at(slot, G, 0, nblk, MODE == kMxDigits ? 0 : c),
+                              a.scales + mx_scale_at(slot, G, 0, nblk, low), a.y + y * a.N, r, c};
+        }
     }
     __syncthreads();
     if (dests == 1 && places[0].row < 0) return;
     if (a.plan.split) {  // the product adds into these rows
         for (int j = 0; j < dests; ++j) {
             if (places[j].row < 0) continue;
-            float* const y = a.y + places[j].y * a.N;
+            float* const y = places[j].y;
             for (int n = blockIdx.y * blockDim.x + threadIdx.x; n < a.N; n += gridDim.y * blockDim.x) y[n] = 0.0f;
         }
     }
@@ -167,23 +176,22 @@ __global__ void __launch_bounds__(kWarps * 32) k_mx_act(const MxAct a) {
         for (int j = 0; j < dests; ++j) {
             const Place p = places[j];
             if (p.row < 0) continue;
-            auto scale = [&](int r, uint32_t w) {
-                *reinterpret_cast<uint32_t*>(a.scales + mx_scale_at(p.slot, G, g, nblk, r)) = w;
-            };
+            const long long sf = (long long)g * nblk * 512;
             if constexpr (MODE == kMxA4) {
-                *reinterpret_cast<uint32_t*>(a.codes + (long long)p.row * (a.K / 2) + g * 64 + 4 * lane) = c;
-                if (lane == 0) scale(p.c, word);
+                *reinterpret_cast<uint32_t*>(p.codes + g * 64 + 4 * lane) = c;
+                if (lane == 0) *reinterpret_cast<uint32_t*>(p.scale + sf) = word;
             } else if constexpr (MODE == kMxParts) {
-                const long long at = (long long)p.row * a.K + g * 128 + 8 * lane;
-                *reinterpret_cast<uint2*>(a.codes + at) = hi;
-                *reinterpret_cast<uint2*>(a.codes + (long long)a.R * a.K + at) = lo;
-                if (lane == 0) scale(p.c, word);
-                if (lane == 1) scale(p.low, lword);
+                uint8_t* const at = p.codes + g * 128 + 8 * lane;
+                *reinterpret_cast<uint2*>(at) = hi;
+                *reinterpret_cast<uint2*>(at + (long long)a.R * a.K) = lo;
+                if (lane == 0) *reinterpret_cast<uint32_t*>(p.scale + sf) = word;
+                if (lane == 1) *reinterpret_cast<uint32_t*>(p.low + sf) = lword;
             } else {
 #pragma unroll
                 for (int k = 0; k < 8; ++k)
-                    *reinterpret_cast<uint32_t*>(a.codes + (8LL * p.row + k) * (a.K / 2) + g * 64 + 4 * lane) = d[k];
-                if (lane < 8) scale(8 * p.c + lane, dword);
+                    *reinterpret_cast<uint32_t*>(p.codes + (long long)k * (a.K / 2) + g * 64 + 4 * lane) = d[k];
+                if (lane < 8)
+                    *reinterpret_cast<uint32_t*>(p.scale + sf + mx_scale_at(0, G, 0, nblk, 8 * p.c + lane)) = dword;
             }
         }
     }
@@ -269,12 +277,19 @@ cudaError_t launch_mx_act(const MxAct& a, cudaStream_t s) {
     // One CTA a row; few rows are cut along K instead, so that their columns are not walked one after another.
     const int rows = a.ids ? a.R / a.topk : a.R, passes = (a.K / 128 + 2 * kWarps - 1) / (2 * kWarps);
     const dim3 grid((unsigned)rows, (unsigned)(rows < 148 ? passes : 1));
-    switch (a.plan.mode) {
-    case kMxA4: k_mx_act<kMxA4><<<grid, kWarps * 32, 0, s>>>(a); break;
-    case kMxDigits: k_mx_act<kMxDigits><<<grid, kWarps * 32, 0, s>>>(a); break;
-    default: k_mx_act<kMxParts><<<grid, kWarps * 32, 0, s>>>(a);
-    }
-    return cudaGetLastError();
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = grid;
+    cfg.blockDim = dim3(kWarps * 32);
+    cfg.stream = s;
+    cudaLaunchAttribute attr[1];
+    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr[0].val.programmaticStreamSerializationAllowed = 1;
+    cfg.attrs = attr;
+    cfg.numAttrs = 1;
+    const cudaError_t e = cudaLaunchKernelEx(&cfg, a.plan.mode == kMxA4       ? k_mx_act<kMxA4>
+                                                   : a.plan.mode == kMxDigits ? k_mx_act<kMxDigits>
+                                                                              : k_mx_act<kMxParts>, a);
+    return e != cudaSuccess ? e : cudaGetLastError();
 }
 
 cudaError_t launch_mx_pack(const uint8_t* codes_in, const uint8_t* scales_in, int N, int K, uint8_t* codes,

@@ -54,7 +54,7 @@ constexpr int TM = 128;              // weight rows per tile
 constexpr int A_BYTES = TM * 128;    // a slot's weight codes
 constexpr int BIG = 64, SMALL = 16;  // rows of the activation boxes
 constexpr int kMaxStages = 12;
-constexpr int kEpiWarp0 = 4, kEpiWarps = 4;
+constexpr int kEpiWarp0 = 4, kEpiWarps = 8;
 constexpr int kThreads = 32 * (kEpiWarp0 + kEpiWarps);
 constexpr uint32_t kTmemCols = 512;
 constexpr int CW = 16;  // accumulator columns per tensor-memory read
@@ -218,19 +218,47 @@ __global__ void __launch_bounds__(kThreads, 1) k_mx_gemm(const __grid_constant__
     // A slot: weight codes, activation codes, weight scales (KBS blocks), activation scales (KBS x nblk blocks).
     const int b_off = A_BYTES, sa_off = p.stage_bytes - KBS * (1 + nblk) * 512, sb_off = sa_off + KBS * 512;
 
-    if (threadIdx.x == 0) {
-        for (int s = 0; s < p.stages; ++s) {
-            mbar_init(bar(B_FULL + s), 2);   // the two producers' expect_tx
-            mbar_init(bar(B_EMPTY + s), 1);  // the step's MMA commit
+    asm volatile("griddepcontrol.launch_dependents;\n" ::: "memory");  // the next call's quantiser may stand by
+    const unsigned long long lim = wait_limit(g.err);
+    bool dead = false;
+    Tile ti;
+    // One step of a tile's weights into ring slot s.
+    auto load_weights = [&](const Tile& t, int k, int s, bool leader) {
+        const int NB = (g.N + TM - 1) / TM;
+        const unsigned sfb = min(KBS, G - k * KBS) * 512;
+        const uint32_t slot = base + s * p.stage_bytes, fb = bar(B_FULL + s);
+        const uint8_t* sf = g.scales + (((long long)t.expert * NB + t.wb) * G + k * KBS) * 512;
+        if (leader) {
+            mbar_expect_tx(fb, (PARTS ? A_BYTES / 2 : A_BYTES) + sfb);  // spread copies count the packed bytes
+            tma_load_2d(slot, &p.tmW, k * 128, t.expert * g.N + t.wb * TM, fb);
+            bulk_load(slot + sa_off, sf, sfb, fb);
         }
-        for (int b = 0; b < 2; ++b) {
-            mbar_init(bar(B_ACCF + b), 1);          // the tile's last commit
-            mbar_init(bar(B_ACCE + b), kEpiWarps);  // one arrive per epilogue warp
+    };
+    int ahead = 0;  // steps of the first tile that warp 0 has issued before the block's first barrier
+
+    if (warp == 0) {
+        const bool leader = elect();
+        if (leader) {
+            for (int s = 0; s < p.stages; ++s) {
+                mbar_init(bar(B_FULL + s), 2);   // the two producers' expect_tx
+                mbar_init(bar(B_EMPTY + s), 1);  // the step's MMA commit
+            }
+            for (int b = 0; b < 2; ++b) {
+                mbar_init(bar(B_ACCF + b), 1);          // the tile's last commit
+                mbar_init(bar(B_ACCE + b), kEpiWarps);  // one arrive per epilogue warp
+            }
+            mbar_init(bar(B_DRAIN), 1);
+            asm volatile("fence.mbarrier_init.release.cluster;\n" ::: "memory");
         }
-        mbar_init(bar(B_DRAIN), 1);
-        asm volatile("fence.mbarrier_init.release.cluster;\n" ::: "memory");
-    }
-    if (warp == 2) {
+        __syncwarp();
+        if (!g.offsets) {  // one weight: its stream starts at once
+            Tiles first(g, cum, KS);
+            if (first.next(ti)) {
+                ahead = min(p.stages, ti.k1 - ti.k0);
+                for (int k = 0; k < ahead; ++k) load_weights(ti, ti.k0 + k, k, leader);
+            }
+        }
+    } else if (warp == 2) {
         asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], %1;\n" ::"r"(smem_u32(&tmem_slot)),
                      "r"(kTmemCols));
         asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;\n");
@@ -262,34 +290,24 @@ __global__ void __launch_bounds__(kThreads, 1) k_mx_gemm(const __grid_constant__
     __syncthreads();
     fence_after();
     const uint32_t tmem = (uint32_t)uniform((int)tmem_slot);
-    const unsigned long long lim = wait_limit(g.err);
-    bool dead = false;
     Tiles tiles(g, cum, KS);
-    Tile ti;
 
     // The three issuing roles run as whole warps, with every operand the same in all lanes, and one elected lane
     // issues: the instructions take their operands from uniform registers, which a lone lane's values would have
     // to be moved to one by one for each of them.
     if (warp == 0) {  // ---- weights ----
         const bool leader = elect();
-        if (leader) asm volatile("prefetch.tensormap [%0];\n" ::"l"(&p.tmW) : "memory");
-        const int NB = (g.N + TM - 1) / TM;
         int step = 0, s = 0, ph = 1;
         while (!dead && tiles.next(ti)) {
-            const int expert = uniform(ti.expert), wb = uniform(ti.wb);
-            const int row = expert * g.N + wb * TM;
-            const uint8_t* sf = g.scales + ((long long)expert * NB + wb) * G * 512;
+            ti.expert = uniform(ti.expert);
+            ti.wb = uniform(ti.wb);
             for (int k = uniform(ti.k0), k1 = uniform(ti.k1); k < k1; ++k, ++step) {
-                if (!__all_sync(kFull, mbar_wait(bar(B_EMPTY + s), ph, lim))) {
-                    dead = true;
-                    break;
-                }
-                const unsigned sfb = min(KBS, G - k * KBS) * 512;
-                const uint32_t slot = base + s * p.stage_bytes, fb = bar(B_FULL + s);
-                if (leader) {
-                    mbar_expect_tx(fb, (PARTS ? A_BYTES / 2 : A_BYTES) + sfb);  // spread copies count the packed bytes
-                    tma_load_2d(slot, &p.tmW, k * 128, row, fb);
-                    bulk_load(slot + sa_off, sf + (long long)k * KBS * 512, sfb, fb);
+                if (step >= ahead) {
+                    if (!__all_sync(kFull, mbar_wait(bar(B_EMPTY + s), ph, lim))) {
+                        dead = true;
+                        break;
+                    }
+                    load_weights(ti, k, s, leader);
                 }
                 if (++s == p.stages) { s = 0; ph ^= 1; }
             }
@@ -385,61 +403,66 @@ __global__ void __launch_bounds__(kThreads, 1) k_mx_gemm(const __grid_constant__
         if (leader) commit(bar(B_DRAIN));
         __all_sync(kFull, mbar_wait(bar(B_DRAIN), 0));
     } else if (warp >= kEpiWarp0) {  // ---- epilogue ----
-        const int q = warp & 3;
+        const int q = warp & 3, h = (warp - kEpiWarp0) >> 2;
+        constexpr int TW = MODE == kMxDigits ? CW / 8 : CW;            // tokens of a tensor-memory read
+        constexpr int READS = kMxRows / mx_planes(MODE) / TW / 2;      // this warp's reads: every second one
+        constexpr int REGS = (READS * TW + 31) / 32;
         asm volatile("griddepcontrol.wait;\n" ::: "memory");  // the quantiser's factors and zeroed outputs
         int tl = 0;
         while (tiles.next(ti)) {
             const int b = tl & 1;
             const int n = ti.wb * TM + 32 * q + lane;
             const uint32_t d = tmem + b * p.acc_cols + ((uint32_t)(32 * q) << 16);
+            const bool part = ti.k1 - ti.k0 < KS;
+            // Before the sums are ready: lane l fetches the output rows (-1: none) of the tokens number
+            // 32 i + l of this warp's.
+            int to[REGS];
+            float factor[REGS];
+#pragma unroll
+            for (int i = 0; i < REGS; ++i) {
+                const int m = 32 * i + lane, c = (2 * (m / TW) + h) * TW + m % TW;
+                to[i] = -1;
+                factor[i] = 1.0f;
+                if (c < ti.rows) {
+                    to[i] = ti.row0 + c;
+                    if constexpr (MODE == kMxDigits) factor[i] = g.xf[to[i]];
+                    if (g.perm) {
+                        to[i] = __ldg(g.perm + to[i]);
+                        if (to[i] >= g.R) to[i] = -1;
+                    }
+                }
+            }
             if (!__all_sync(kFull, mbar_wait(bar(B_ACCF + b), (tl >> 1) & 1, lim))) {  // together
                 dead = true;
                 break;
             }
             fence_after();
-            const bool part = ti.k1 - ti.k0 < KS, mine = n < g.N;
-            constexpr int TW = MODE == kMxDigits ? CW / 8 : CW;  // tokens of a read
-            for (int c0 = 0; c0 < ti.rows; c0 += TW) {
+#pragma unroll
+            for (int j = 0; j < READS; ++j) {
+                const int c0 = (2 * j + h) * TW;
+                if (c0 >= ti.rows) break;
                 uint32_t v[CW], lo[CW];
                 tmem_ld16(d + (MODE == kMxDigits ? 8 : 1) * c0, v);
                 if constexpr (PARTS) tmem_ld16(d + mx_pad16(ti.rows) + c0, lo);
-                // Lane i: the output row of the read's token i, -1 past the block.
-                int to = -1;
-                float factor = 1.0f;
-                if (lane < TW && c0 + lane < ti.rows) {
-                    to = ti.row0 + c0 + lane;
-                    if constexpr (MODE == kMxDigits) factor = g.xf[to];
-                    if (g.perm) {
-                        to = __ldg(g.perm + to);
-                        if (to >= g.R) to = -1;
-                    }
-                }
                 tmem_wait_ld();
-                float f[TW];
 #pragma unroll
                 for (int i = 0; i < TW; ++i) {
+                    const int m = j * TW + i;
+                    const int row = __shfl_sync(kFull, to[m / 32], m % 32);
+                    float f = __uint_as_float(v[i]);
+                    if constexpr (PARTS) f += __uint_as_float(lo[i]);
                     if constexpr (MODE == kMxDigits) {  // small digits first
-                        const float* w = reinterpret_cast<const float*>(v + 8 * i);
-                        f[i] = ((w[0] + w[1]) + ((w[2] + w[3]) + ((w[4] + w[5]) + (w[6] + w[7])))) *
-                               __shfl_sync(kFull, factor, i);
-                    } else {
-                        f[i] = __uint_as_float(v[i]);
-                        if constexpr (PARTS) f[i] += __uint_as_float(lo[i]);
+                        const uint32_t* w = v + 8 * i;
+                        f = ((__uint_as_float(w[0]) + __uint_as_float(w[1])) +
+                             ((__uint_as_float(w[2]) + __uint_as_float(w[3])) +
+                              ((__uint_as_float(w[4]) + __uint_as_float(w[5])) +
+                               (__uint_as_float(w[6]) + __uint_as_float(w[7]))))) *
+                            __shfl_sync(kFull, factor[m / 32], m % 32);
                     }
-                }
-                if (!g.perm && !part && c0 + TW <= ti.rows) {  // the common case: rows one after another
-                    float* y = g.y + (long long)(ti.row0 + c0) * g.N + n;
-#pragma unroll
-                    for (int i = 0; i < TW; ++i, y += g.N)
-                        if (mine) *y = f[i];
-                } else {
-#pragma unroll
-                    for (int i = 0; i < TW; ++i) {
-                        const int row = __shfl_sync(kFull, to, i);
-                        float* const y = g.y + (long long)row * g.N + n;
-                        if (row < 0 || !mine) continue;
-                        if (part) atomicAdd(y, f[i]);
-                        else *y = f[i];
+                    float* const y = g.y + (long long)row * g.N + n;
+                    if (row >= 0 && n < g.N) {
+                        if (part) atomicAdd(y, f);
+                        else *y = f;
                     }
                 }
             }
