@@ -12,6 +12,7 @@ helpers, which return integers.
 from __future__ import annotations
 
 import ctypes
+from functools import lru_cache
 from pathlib import Path
 
 import torch
@@ -128,19 +129,30 @@ def _ptr(t: torch.Tensor | None):
         raise ValueError("expected a CUDA tensor")
     if not t.is_contiguous():
         raise ValueError("expected a contiguous tensor")
-    return ctypes.c_void_p(t.data_ptr())
+    return t.data_ptr()
 
 
 def _stream(stream=None):
-    s = torch.cuda.current_stream() if stream is None else stream
-    return ctypes.c_void_p(s.cuda_stream)
+    """Address of the stream, or of the current device's current one."""
+    if stream is not None:
+        return stream.cuda_stream
+    return torch._C._cuda_getCurrentRawStream(torch._C._cuda_getDevice())
+
+
+def _on(device, fn, *args, stream=None) -> int:
+    """fn(*args, stream) on the tensors' device, whichever device is the current one."""
+    if device.index == torch._C._cuda_getDevice():
+        return fn(*args, _stream(stream))
+    with torch.cuda.device(device):
+        return fn(*args, _stream(stream))
 
 
 def _empty(nbytes: int, device) -> torch.Tensor:
     return torch.empty(max(int(nbytes), 16), dtype=torch.uint8, device=device)
 
 
-# ---- sizes ------------------------------------------------------------------------
+# ---- sizes: functions of their arguments alone, remembered so that a call does not ask again ----------
+@lru_cache(maxsize=4096)
 def qlinear_packed_sizes(fmt: int, N: int, K: int):
     c, s, z = ctypes.c_size_t(), ctypes.c_size_t(), ctypes.c_size_t()
     _check("qlinear_packed_sizes", lib().qlinear_packed_sizes(fmt, N, K, ctypes.byref(c), ctypes.byref(s),
@@ -148,6 +160,7 @@ def qlinear_packed_sizes(fmt: int, N: int, K: int):
     return c.value, s.value, z.value
 
 
+@lru_cache(maxsize=4096)
 def qlinear_workspace_size(fmt: int, flags: int, M: int, N: int, K: int) -> int:
     b = ctypes.c_size_t()
     _check("qlinear_workspace_size", lib().qlinear_workspace_size(fmt, flags, M, N, K, ctypes.byref(b)))
@@ -158,6 +171,7 @@ def _experts_struct(E, N, K, fmt, flags, codes, scales):
     return ql_experts(E, N, K, fmt, flags, codes.data_ptr(), scales.data_ptr())
 
 
+@lru_cache(maxsize=4096)
 def moe_workspace_size(E: int, N: int, K: int, fmt: int, flags: int, T: int, topk: int) -> int:
     ex = ql_experts(E, N, K, fmt, flags, 32, 32)  # placeholder aligned pointers: only sizes are read
     b = ctypes.c_size_t()
@@ -197,8 +211,8 @@ def qlinear_forward(x: torch.Tensor, codes: torch.Tensor, scales: torch.Tensor, 
     need = qlinear_workspace_size(fmt, flags, M, N, K)
     if ws is None or ws.numel() < need:
         ws = _empty(need, x.device)
-    st = lib().qlinear_forward(_ptr(x), _ptr(codes), _ptr(scales), _ptr(zeros), fmt, flags, M, N, K, _ptr(y),
-                               _ptr(ws), ws.numel(), _stream(stream))
+    st = _on(x.device, lib().qlinear_forward, _ptr(x), _ptr(codes), _ptr(scales), _ptr(zeros), fmt, flags, M, N, K,
+             _ptr(y), _ptr(ws), ws.numel(), stream=stream)
     _check("qlinear_forward", st)
     return y
 
@@ -283,10 +297,9 @@ def act_quant_mxfp4(x: torch.Tensor, rotate: bool = False, stream=None):
     M, K = _rows(x, "act_quant_mxfp4")
     cb, sb, _ = qlinear_packed_sizes(MXFP4_G32, M, K)
     codes, scales = _empty(cb, x.device), _empty(sb, x.device)
-    with torch.cuda.device(x.device):
-        _check("act_quant_mxfp4", lib().act_quant_mxfp4(_ptr(x), M, K, int(rotate), _ptr(codes), _ptr(scales),
-                                                        _stream(stream)))
-    return codes[:cb], scales[:sb]
+    _check("act_quant_mxfp4", _on(x.device, lib().act_quant_mxfp4, _ptr(x), M, K, int(rotate), _ptr(codes),
+                                  _ptr(scales), stream=stream))
+    return codes, scales
 
 
 def mxfp4_dequant(codes: torch.Tensor, scales: torch.Tensor, N: int, K: int, out: torch.Tensor | None = None,
@@ -299,8 +312,8 @@ def mxfp4_dequant(codes: torch.Tensor, scales: torch.Tensor, N: int, K: int, out
         out = torch.empty((N, K), dtype=torch.bfloat16, device=codes.device)
     elif out.dtype != torch.bfloat16 or tuple(out.shape) != (N, K):
         raise ValueError(f"out must be a bf16 tensor of shape ({N}, {K})")
-    with torch.cuda.device(codes.device):
-        _check("mxfp4_dequant", lib().mxfp4_dequant(_ptr(codes), _ptr(scales), N, K, _ptr(out), _stream(stream)))
+    _check("mxfp4_dequant", _on(codes.device, lib().mxfp4_dequant, _ptr(codes), _ptr(scales), N, K, _ptr(out),
+                                stream=stream))
     return out
 
 
@@ -330,18 +343,18 @@ def moe_gate_up(x: torch.Tensor, topk_ids: torch.Tensor, codes: torch.Tensor, sc
     T, K = x.shape
     topk = topk_ids.shape[1]
     ex = _experts_struct(E, N, K, fmt, flags, codes, scales)
-    b = ctypes.c_size_t()
-    _check("moe_workspace_size", lib().moe_workspace_size(ctypes.byref(ex), T, topk, ctypes.byref(b)))
-    if ws is None or ws.numel() < b.value:
-        ws = _empty(b.value, x.device)
+    need = moe_workspace_size(E, N, K, fmt, flags, T, topk)
+    if ws is None or ws.numel() < need:
+        ws = _empty(need, x.device)
     if y is None:
         y = torch.empty((T, topk, N), dtype=torch.float32, device=x.device)
-    st = lib().moe_gate_up(_ptr(x), _ptr(topk_ids), _ptr(topk_weights), ctypes.byref(ex), T, topk, _ptr(y),
-                           _ptr(ws), ws.numel(), _stream(stream))
+    st = _on(x.device, lib().moe_gate_up, _ptr(x), _ptr(topk_ids), _ptr(topk_weights), ctypes.byref(ex), T, topk,
+             _ptr(y), _ptr(ws), ws.numel(), stream=stream)
     _check("moe_gate_up", st)
     return y
 
 
+@lru_cache(maxsize=4096)
 def qlinear_grouped_workspace_size(E: int, N: int, K: int, fmt: int, flags: int, R: int) -> int:
     ex = ql_experts(E, N, K, fmt, flags, 32, 32)  # placeholder aligned pointers: only sizes are read
     b = ctypes.c_size_t()
@@ -370,9 +383,8 @@ def qlinear_grouped(x: torch.Tensor, offsets: torch.Tensor, codes: torch.Tensor,
     elif y.dtype != torch.float32 or tuple(y.shape) != (R, N):
         raise ValueError(f"y must be an fp32 tensor of shape ({R}, {N})")
     ex = _experts_struct(E, N, K, fmt, flags, codes, scales)
-    with torch.cuda.device(x.device):
-        _check("qlinear_grouped", lib().qlinear_grouped(_ptr(x), _ptr(offsets), ctypes.byref(ex), R, _ptr(y), _ptr(ws),
-                                                        ws.numel() * ws.element_size(), _stream(stream)))
+    _check("qlinear_grouped", _on(x.device, lib().qlinear_grouped, _ptr(x), _ptr(offsets), ctypes.byref(ex), R,
+                                  _ptr(y), _ptr(ws), ws.numel() * ws.element_size(), stream=stream))
     return y
 
 
