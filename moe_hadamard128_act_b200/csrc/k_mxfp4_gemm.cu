@@ -44,23 +44,13 @@
 // All waits are bounded; on a timeout the CTA sets QL_DEVERR_TIMEOUT and winds
 // down without leaving tensor memory allocated, MMAs running or copies in
 // flight.
-#include "mx_layout.cuh"
-#include "ql_internal.h"
+#include "mx_gemm.cuh"
 
 namespace ql {
 namespace {
 
-constexpr int TM = 128;              // weight rows per tile
-constexpr int A_BYTES = TM * 128;    // a slot's weight codes
-constexpr int BIG = 64, SMALL = 16;  // rows of the activation boxes
-constexpr int kMaxStages = 12;
-constexpr int kEpiWarp0 = 4, kEpiWarps = 8;
-constexpr int kThreads = 32 * (kEpiWarp0 + kEpiWarps);
-constexpr uint32_t kTmemCols = 512;
-constexpr int CW = 16;  // accumulator columns per tensor-memory read
 constexpr int B_FULL = 0, B_EMPTY = kMaxStages, B_ACCF = 2 * kMaxStages, B_ACCE = B_ACCF + 2, B_DRAIN = B_ACCE + 2,
               NBARS = B_DRAIN + 1;
-constexpr int kSmemMax = 227 * 1024;
 
 struct MxParams {
     CUtensorMap tmW;         // weight codes: [E * N rows], box [128 rows][128 bytes of shared memory]
@@ -70,21 +60,6 @@ struct MxParams {
     int acc_cols, sf0, sf_cols;  // tensor memory: accumulator stride, first scale column, scale columns per slot
 };
 
-__device__ __forceinline__ uint64_t desc_sw128(uint32_t addr) {
-    // K-major, 128-byte swizzle: 8-row atoms 1024 bytes apart (SBO), version 1.
-    return (uint64_t)((addr >> 4) & 0x3FFFu) | (1ull << 16) | (64ull << 32) | (1ull << 46) | (2ull << 61);
-}
-__device__ __forceinline__ uint64_t desc_scales(uint32_t addr) {
-    // No swizzle: 8 rows of 16 bytes, 128 bytes apart.
-    return (uint64_t)((addr >> 4) & 0x3FFFu) | (1ull << 16) | (8ull << 32) | (1ull << 46);
-}
-// Block-scaled kinds: A format at bits 7-9, B format at 10-12, N >> 3 at 17-22, scales UE8M0 (bit 23), M >> 7 at
-// 27-28; the scales' byte within a tensor-memory word at 4-5 (B) and 29-30 (A).
-template <int MODE>
-__device__ __forceinline__ uint32_t idesc(int n) {
-    const uint32_t fmt = MODE == kMxParts ? (5u << 7) : (1u << 7) | (1u << 10);  // E2M1 x E4M3, or E2M1 x E2M1
-    return fmt | ((uint32_t)(n >> 3) << 17) | (1u << 23) | ((uint32_t)(TM >> 7) << 27);
-}
 template <int MODE>
 __device__ __forceinline__ void mma(uint32_t d, uint64_t ad, uint64_t bd, uint32_t id, uint32_t sfa, uint32_t sfb,
                                     uint32_t acc_in) {
@@ -107,100 +82,6 @@ __device__ __forceinline__ void commit(uint32_t bar) {
     asm volatile("tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0];\n" ::"r"(bar)
                  : "memory");
 }
-__device__ __forceinline__ void fence_after() { asm volatile("tcgen05.fence::after_thread_sync;\n" ::: "memory"); }
-__device__ __forceinline__ void fence_before() { asm volatile("tcgen05.fence::before_thread_sync;\n" ::: "memory"); }
-__device__ __forceinline__ void arrive(uint32_t bar) {
-    asm volatile("mbarrier.arrive.shared::cta.b64 _, [%0];\n" ::"r"(bar) : "memory");
-}
-__device__ __forceinline__ void tmem_ld16(uint32_t addr, uint32_t r[CW]) {
-    asm volatile(
-        "tcgen05.ld.sync.aligned.32x32b.x16.b32 {%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15}, [%16];\n"
-        : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7]),
-          "=r"(r[8]), "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]), "=r"(r[14]), "=r"(r[15])
-        : "r"(addr)
-        : "memory");
-}
-__device__ __forceinline__ void tmem_wait_ld() { asm volatile("tcgen05.wait::ld.sync.aligned;\n" ::: "memory"); }
-
-// One lane of a converged warp, the same every time.
-__device__ __forceinline__ bool elect() {
-    uint32_t p;
-    asm volatile("{\n .reg .pred p;\n elect.sync _|p, 0xffffffff;\n selp.u32 %0, 1, 0, p;\n}\n" : "=r"(p));
-    return p != 0;
-}
-__device__ __forceinline__ int uniform(int v) { return __shfl_sync(kFull, v, 0); }
-
-// Accumulator columns of a block of `rows` tokens.
-template <int MODE>
-__device__ __forceinline__ int columns(int rows) {
-    return MODE == kMxParts ? 2 * mx_pad16(rows) : mx_pad16(mx_planes(MODE) * rows);
-}
-
-struct Tile {
-    int expert, row0, rows, wb, slot;
-    int k0, k1;  // its steps
-};
-
-// The CTA's tiles, each role walking the same list: weight block by weight block within an expert so that its
-// token blocks share the weights in L2; cum[e]: token blocks of the experts before e.
-struct Tiles {
-    const MxGemm& g;
-    const int* cum;
-    int NB, KS, total, t;
-    long long u, end;  // split: the CTA's run of steps
-    __device__ Tiles(const MxGemm& g_, const int* cum_, int KS_)
-        : g(g_), cum(cum_), NB((g_.N + TM - 1) / TM), KS(KS_), t(blockIdx.x), u(-1), end(0) {
-        total = NB * (g.offsets ? cum[g.E] : (g.R + g.plan.nt - 1) / g.plan.nt);
-        const int ctas = gridDim.x;
-        // Runs of whole tiles lose up to a tile's time in the last round; past eight rounds that is little.
-        if (g.plan.split && (2 * total <= ctas || (total > ctas && total < 8 * ctas && total % ctas))) {
-            const int parts = 2 * total <= ctas ? 2 * total : ctas;
-            const long long steps = (long long)total * KS, c = blockIdx.x;
-            u = c < parts ? c * steps / parts : 0;
-            end = c < parts ? (c + 1) * steps / parts : 0;
-        }
-    }
-    __device__ bool next(Tile& o) {
-        int tile = t;
-        o.k0 = 0;
-        o.k1 = KS;
-        if (u >= 0) {
-            if (u >= end) return false;
-            tile = (int)(u / KS);
-            o.k0 = (int)(u - (long long)tile * KS);
-            o.k1 = (int)min((long long)KS, o.k0 + (end - u));
-            u += o.k1 - o.k0;
-        } else {
-            if (t >= total) return false;
-            t += gridDim.x;
-        }
-        int e = 0, i, first = 0, count = g.R;
-        if (g.offsets) {
-            int hi = g.E;  // the largest e with cum[e] * NB <= tile
-            while (hi - e > 1) {
-                const int m = (e + hi) >> 1;
-                if (cum[m] * NB <= tile) e = m;
-                else hi = m;
-            }
-            const int nb = cum[e + 1] - cum[e], local = tile - cum[e] * NB;
-            o.wb = local / nb;
-            i = local - o.wb * nb;
-            int last;
-            mx_segment(g.offsets, e, g.R, first, last);
-            count = last - first;
-        } else {
-            const int nb = (g.R + g.plan.nt - 1) / g.plan.nt;
-            o.wb = tile / nb;
-            i = tile - o.wb * nb;
-        }
-        o.expert = e;
-        o.row0 = first + i * g.plan.nt;
-        o.rows = min(g.plan.nt, count - i * g.plan.nt);
-        o.slot = first / g.plan.nt + e + i;
-        return true;
-    }
-};
-
 template <int MODE>
 __global__ void __launch_bounds__(kThreads, 1) k_mx_gemm(const __grid_constant__ MxParams p) {
     extern __shared__ uint8_t smem_raw[];
@@ -252,7 +133,7 @@ __global__ void __launch_bounds__(kThreads, 1) k_mx_gemm(const __grid_constant__
         }
         __syncwarp();
         if (!g.offsets) {  // one weight: its stream starts at once
-            Tiles first(g, cum, KS);
+            Tiles<TM> first(g, cum, KS, blockIdx.x, gridDim.x, g.plan.split);
             if (first.next(ti)) {
                 ahead = min(p.stages, ti.k1 - ti.k0);
                 for (int k = 0; k < ahead; ++k) load_weights(ti, ti.k0 + k, k, leader);
@@ -263,34 +144,12 @@ __global__ void __launch_bounds__(kThreads, 1) k_mx_gemm(const __grid_constant__
                      "r"(kTmemCols));
         asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;\n");
     }
-    if (g.offsets) {  // token blocks of each expert, then their exclusive sums
-        for (int e = threadIdx.x; e < g.E; e += kThreads) {
-            int a, b;
-            if (!mx_segment(g.offsets, e, g.R, a, b)) atomicOr(g.err, (unsigned)QL_DEVERR_BOUNDS);
-            cum[e] = (b - a + g.plan.nt - 1) / g.plan.nt;
-        }
-        __syncthreads();
-        if (warp == 3) {
-            int sum = 0;
-            for (int e0 = 0; e0 < g.E; e0 += 32) {
-                const int v = e0 + lane < g.E ? cum[e0 + lane] : 0;
-                int incl = v;
-#pragma unroll
-                for (int d = 1; d < 32; d <<= 1) {
-                    const int up = __shfl_up_sync(kFull, incl, d);
-                    if (lane >= d) incl += up;
-                }
-                if (e0 + lane < g.E) cum[e0 + lane] = sum + incl - v;
-                sum += __shfl_sync(kFull, incl, 31);
-            }
-            if (lane == 0) cum[g.E] = sum;
-        }
-    }
+    if (g.offsets) count_blocks(g, cum, warp, lane);
     fence_before();
     __syncthreads();
     fence_after();
     const uint32_t tmem = (uint32_t)uniform((int)tmem_slot);
-    Tiles tiles(g, cum, KS);
+    Tiles<TM> tiles(g, cum, KS, blockIdx.x, gridDim.x, g.plan.split);
 
     // The three issuing roles run as whole warps, with every operand the same in all lanes, and one elected lane
     // issues: the instructions take their operands from uniform registers, which a lone lane's values would have
@@ -361,7 +220,7 @@ __global__ void __launch_bounds__(kThreads, 1) k_mx_gemm(const __grid_constant__
                 dead = true;
                 break;
             }
-            const uint32_t d = tmem + b * p.acc_cols, id0 = idesc<MODE>(uniform(columns<MODE>(ti.rows)));
+            const uint32_t d = tmem + b * p.acc_cols, id0 = idesc<MODE>(TM, uniform(columns<MODE>(ti.rows)));
             const int k0 = uniform(ti.k0), k1 = uniform(ti.k1);
             for (int k = k0; k < k1; ++k) {
                 if (!__all_sync(kFull, mbar_wait(bar(B_FULL + s), ph, lim))) {
@@ -404,68 +263,19 @@ __global__ void __launch_bounds__(kThreads, 1) k_mx_gemm(const __grid_constant__
         __all_sync(kFull, mbar_wait(bar(B_DRAIN), 0));
     } else if (warp >= kEpiWarp0) {  // ---- epilogue ----
         const int q = warp & 3, h = (warp - kEpiWarp0) >> 2;
-        constexpr int TW = MODE == kMxDigits ? CW / 8 : CW;            // tokens of a tensor-memory read
-        constexpr int READS = kMxRows / mx_planes(MODE) / TW / 2;      // this warp's reads: every second one
-        constexpr int REGS = (READS * TW + 31) / 32;
         asm volatile("griddepcontrol.wait;\n" ::: "memory");  // the quantiser's factors and zeroed outputs
         int tl = 0;
         while (tiles.next(ti)) {
             const int b = tl & 1;
-            const int n = ti.wb * TM + 32 * q + lane;
-            const uint32_t d = tmem + b * p.acc_cols + ((uint32_t)(32 * q) << 16);
-            const bool part = ti.k1 - ti.k0 < KS;
-            // Before the sums are ready: lane l fetches the output rows (-1: none) of the tokens number
-            // 32 i + l of this warp's.
-            int to[REGS];
-            float factor[REGS];
-#pragma unroll
-            for (int i = 0; i < REGS; ++i) {
-                const int m = 32 * i + lane, c = (2 * (m / TW) + h) * TW + m % TW;
-                to[i] = -1;
-                factor[i] = 1.0f;
-                if (c < ti.rows) {
-                    to[i] = ti.row0 + c;
-                    if constexpr (MODE == kMxDigits) factor[i] = g.xf[to[i]];
-                    if (g.perm) {
-                        to[i] = __ldg(g.perm + to[i]);
-                        if (to[i] >= g.R) to[i] = -1;
-                    }
-                }
-            }
+            Epilogue<MODE> epi;
+            epi.fetch(g, ti, h, lane);
             if (!__all_sync(kFull, mbar_wait(bar(B_ACCF + b), (tl >> 1) & 1, lim))) {  // together
                 dead = true;
                 break;
             }
             fence_after();
-#pragma unroll
-            for (int j = 0; j < READS; ++j) {
-                const int c0 = (2 * j + h) * TW;
-                if (c0 >= ti.rows) break;
-                uint32_t v[CW], lo[CW];
-                tmem_ld16(d + (MODE == kMxDigits ? 8 : 1) * c0, v);
-                if constexpr (PARTS) tmem_ld16(d + mx_pad16(ti.rows) + c0, lo);
-                tmem_wait_ld();
-#pragma unroll
-                for (int i = 0; i < TW; ++i) {
-                    const int m = j * TW + i;
-                    const int row = __shfl_sync(kFull, to[m / 32], m % 32);
-                    float f = __uint_as_float(v[i]);
-                    if constexpr (PARTS) f += __uint_as_float(lo[i]);
-                    if constexpr (MODE == kMxDigits) {  // small digits first
-                        const uint32_t* w = v + 8 * i;
-                        f = ((__uint_as_float(w[0]) + __uint_as_float(w[1])) +
-                             ((__uint_as_float(w[2]) + __uint_as_float(w[3])) +
-                              ((__uint_as_float(w[4]) + __uint_as_float(w[5])) +
-                               (__uint_as_float(w[6]) + __uint_as_float(w[7]))))) *
-                            __shfl_sync(kFull, factor[m / 32], m % 32);
-                    }
-                    float* const y = g.y + (long long)row * g.N + n;
-                    if (row >= 0 && n < g.N) {
-                        if (part) atomicAdd(y, f);
-                        else *y = f;
-                    }
-                }
-            }
+            epi.store(g, ti, tmem + b * p.acc_cols + ((uint32_t)(32 * q) << 16), h, ti.wb * TM + 32 * q + lane,
+                      ti.k1 - ti.k0 < KS);
             fence_before();
             __syncwarp();
             if (lane == 0) arrive(bar(B_ACCE + b));
@@ -496,8 +306,8 @@ cudaError_t run(const MxGemm& g, cudaStream_t s) {
     p.acc_cols = (int)align_up(rows, 32);
     p.sf0 = 2 * p.acc_cols;
     p.sf_cols = KBS * 4 * (1 + nblk);
-    const int smem_max = (int)(di.smem_optin < (size_t)kSmemMax ? di.smem_optin : kSmemMax) - 8 * 1024;
-    p.stages = (smem_max - 1024) / p.stage_bytes;
+    if (di.smem_optin < (size_t)kSmemMax + 8 * 1024) return cudaErrorInvalidValue;
+    p.stages = (kSmemMax - 1024) / p.stage_bytes;
     if (p.stages > ((int)kTmemCols - p.sf0) / p.sf_cols) p.stages = ((int)kTmemCols - p.sf0) / p.sf_cols;
     if (p.stages > kMaxStages) p.stages = kMaxStages;
     if (p.stages < 2) return cudaErrorInvalidValue;
@@ -513,7 +323,7 @@ cudaError_t run(const MxGemm& g, cudaStream_t s) {
     int dev = 0;
     cudaGetDevice(&dev);
     if (dev >= 64 || !attr_set[dev]) {
-        e = cudaFuncSetAttribute(k_mx_gemm<MODE>, cudaFuncAttributeMaxDynamicSharedMemorySize, kSmemMax - 8 * 1024);
+        e = cudaFuncSetAttribute(k_mx_gemm<MODE>, cudaFuncAttributeMaxDynamicSharedMemorySize, kSmemMax);
         if (e != cudaSuccess) return e;
         if (dev < 64) attr_set[dev] = true;
     }
@@ -551,10 +361,14 @@ MxPlan mx_plan(bool a16, int R, int N, int K, int E, int sms) {
     // Cutting tiles along K costs a zeroed y: worth it while y is small beside the weights.
     const long long tiles = (long long)((N + TM - 1) / TM) * mx_slots(R, 0, p.nt);
     p.split = (long long)R * N * 4 <= (4 << 20) && (E || tiles < 8LL * sms);
+    // Two CTAs to a tile once a token block is wide enough for its operand stream to count.
+    p.pair = p.mode != kMxDigits && p.nt * P >= 64;
+    if (p.pair) p.split = 0;
     return p;
 }
 
 cudaError_t launch_mx_gemm(const MxGemm& g, cudaStream_t s) {
+    if (g.plan.pair) return launch_mx_pair(g, s);
     switch (g.plan.mode) {
     case kMxA4: return run<kMxA4>(g, s);
     case kMxDigits: return run<kMxDigits>(g, s);

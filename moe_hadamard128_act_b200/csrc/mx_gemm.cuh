@@ -1,0 +1,221 @@
+// mx_gemm.cuh -- what the two MXFP4 product kernels share: descriptors of the
+// block-scaled tensor-core instructions, the list of tiles that every role of a
+// kernel walks, and the epilogue.
+#pragma once
+
+#include "mx_layout.cuh"
+
+namespace ql {
+namespace {
+
+constexpr int TM = 128;              // weight rows per CTA and tile: tensor-memory lanes
+constexpr int A_BYTES = TM * 128;    // a step's weight codes
+constexpr int BIG = 64, SMALL = 16;  // rows of the activation boxes
+constexpr int kMaxStages = 12;
+constexpr int kEpiWarp0 = 4, kEpiWarps = 8;
+constexpr int kThreads = 32 * (kEpiWarp0 + kEpiWarps);
+constexpr uint32_t kTmemCols = 512;
+constexpr int CW = 16;  // accumulator columns per tensor-memory read
+constexpr int kSmemMax = 219 * 1024;  // dynamic shared memory of a CTA at most
+
+__device__ __forceinline__ uint64_t desc_sw128(uint32_t addr) {
+    // K-major, 128-byte swizzle: 8-row atoms 1024 bytes apart (SBO), version 1.
+    return (uint64_t)((addr >> 4) & 0x3FFFu) | (1ull << 16) | (64ull << 32) | (1ull << 46) | (2ull << 61);
+}
+__device__ __forceinline__ uint64_t desc_scales(uint32_t addr) {
+    // No swizzle: 8 rows of 16 bytes, 128 bytes apart.
+    return (uint64_t)((addr >> 4) & 0x3FFFu) | (1ull << 16) | (8ull << 32) | (1ull << 46);
+}
+// Block-scaled kinds: A format at bits 7-9, B format at 10-12, N >> 3 at 17-22, scales UE8M0 (bit 23), M >> 7 at
+// 27-28; the scales' byte within a tensor-memory word at 4-5 (B) and 29-30 (A).
+template <int MODE>
+__device__ __forceinline__ uint32_t idesc(int m, int n) {
+    const uint32_t fmt = MODE == kMxParts ? (5u << 7) : (1u << 7) | (1u << 10);  // E2M1 x E4M3, or E2M1 x E2M1
+    return fmt | ((uint32_t)(n >> 3) << 17) | (1u << 23) | ((uint32_t)(m >> 7) << 27);
+}
+__device__ __forceinline__ void fence_after() { asm volatile("tcgen05.fence::after_thread_sync;\n" ::: "memory"); }
+__device__ __forceinline__ void fence_before() { asm volatile("tcgen05.fence::before_thread_sync;\n" ::: "memory"); }
+__device__ __forceinline__ void arrive(uint32_t bar) {
+    asm volatile("mbarrier.arrive.shared::cta.b64 _, [%0];\n" ::"r"(bar) : "memory");
+}
+__device__ __forceinline__ void tmem_ld16(uint32_t addr, uint32_t r[CW]) {
+    asm volatile(
+        "tcgen05.ld.sync.aligned.32x32b.x16.b32 {%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15}, [%16];\n"
+        : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7]),
+          "=r"(r[8]), "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]), "=r"(r[14]), "=r"(r[15])
+        : "r"(addr)
+        : "memory");
+}
+__device__ __forceinline__ void tmem_wait_ld() { asm volatile("tcgen05.wait::ld.sync.aligned;\n" ::: "memory"); }
+
+// One lane of a converged warp, the same every time.
+__device__ __forceinline__ bool elect() {
+    uint32_t p;
+    asm volatile("{\n .reg .pred p;\n elect.sync _|p, 0xffffffff;\n selp.u32 %0, 1, 0, p;\n}\n" : "=r"(p));
+    return p != 0;
+}
+__device__ __forceinline__ int uniform(int v) { return __shfl_sync(kFull, v, 0); }
+
+// Accumulator columns of a block of `rows` tokens.
+template <int MODE>
+__device__ __forceinline__ int columns(int rows) {
+    return MODE == kMxParts ? 2 * mx_pad16(rows) : mx_pad16(mx_planes(MODE) * rows);
+}
+
+struct Tile {
+    int expert, row0, rows, wb, slot;
+    int k0, k1;  // its steps
+};
+
+// The tiles of unit `id` of `units` (a CTA, or a pair of them), each role walking the same list: weight block (of
+// TR rows) by weight block within an expert so that its token blocks share the weights in L2; cum[e]: token blocks
+// of the experts before e.  With `split` tiles may be cut along K between two units.
+template <int TR>
+struct Tiles {
+    const MxGemm& g;
+    const int* cum;
+    int NB, KS, units, total, t;
+    long long u, end;  // split: the unit's run of steps
+    __device__ Tiles(const MxGemm& g_, const int* cum_, int KS_, int id, int units_, bool split)
+        : g(g_), cum(cum_), NB((g_.N + TR - 1) / TR), KS(KS_), units(units_), t(id), u(-1), end(0) {
+        total = NB * (g.offsets ? cum[g.E] : (g.R + g.plan.nt - 1) / g.plan.nt);
+        // Runs of whole tiles lose up to a tile's time in the last round; past eight rounds that is little.
+        if (split && (2 * total <= units || (total > units && total < 8 * units && total % units))) {
+            const int parts = 2 * total <= units ? 2 * total : units;
+            const long long steps = (long long)total * KS, c = id;
+            u = c < parts ? c * steps / parts : 0;
+            end = c < parts ? (c + 1) * steps / parts : 0;
+        }
+    }
+    __device__ bool next(Tile& o) {
+        int tile = t;
+        o.k0 = 0;
+        o.k1 = KS;
+        if (u >= 0) {
+            if (u >= end) return false;
+            tile = (int)(u / KS);
+            o.k0 = (int)(u - (long long)tile * KS);
+            o.k1 = (int)min((long long)KS, o.k0 + (end - u));
+            u += o.k1 - o.k0;
+        } else {
+            if (t >= total) return false;
+            t += units;
+        }
+        int e = 0, i, first = 0, count = g.R;
+        if (g.offsets) {
+            int hi = g.E;  // the largest e with cum[e] * NB <= tile
+            while (hi - e > 1) {
+                const int m = (e + hi) >> 1;
+                if (cum[m] * NB <= tile) e = m;
+                else hi = m;
+            }
+            const int nb = cum[e + 1] - cum[e], local = tile - cum[e] * NB;
+            o.wb = local / nb;
+            i = local - o.wb * nb;
+            int last;
+            mx_segment(g.offsets, e, g.R, first, last);
+            count = last - first;
+        } else {
+            const int nb = (g.R + g.plan.nt - 1) / g.plan.nt;
+            o.wb = tile / nb;
+            i = tile - o.wb * nb;
+        }
+        o.expert = e;
+        o.row0 = first + i * g.plan.nt;
+        o.rows = min(g.plan.nt, count - i * g.plan.nt);
+        o.slot = first / g.plan.nt + e + i;
+        return true;
+    }
+};
+
+// Token blocks of each expert, then their exclusive sums: cum[e], e <= E.  By the whole CTA; the sums are there
+// after the caller's next barrier.
+__device__ __forceinline__ void count_blocks(const MxGemm& g, int* cum, int warp, int lane) {
+    for (int e = threadIdx.x; e < g.E; e += kThreads) {
+        int a, b;
+        if (!mx_segment(g.offsets, e, g.R, a, b)) atomicOr(g.err, (unsigned)QL_DEVERR_BOUNDS);
+        cum[e] = (b - a + g.plan.nt - 1) / g.plan.nt;
+    }
+    __syncthreads();
+    if (warp != 3) return;
+    int sum = 0;
+    for (int e0 = 0; e0 < g.E; e0 += 32) {
+        const int v = e0 + lane < g.E ? cum[e0 + lane] : 0;
+        int incl = v;
+#pragma unroll
+        for (int d = 1; d < 32; d <<= 1) {
+            const int up = __shfl_up_sync(kFull, incl, d);
+            if (lane >= d) incl += up;
+        }
+        if (e0 + lane < g.E) cum[e0 + lane] = sum + incl - v;
+        sum += __shfl_sync(kFull, incl, 31);
+    }
+    if (lane == 0) cum[g.E] = sum;
+}
+
+// The epilogue of one tile in two halves, for warp kEpiWarp0 + w: lanes 32 (w % 4) .. + 31 of the accumulator are
+// weight rows, i.e. consecutive outputs of a token; the two warps of a lane quarter take every second read.
+template <int MODE>
+struct Epilogue {
+    static constexpr bool PARTS = MODE == kMxParts;
+    static constexpr int TW = MODE == kMxDigits ? CW / 8 : CW;        // tokens of a tensor-memory read
+    static constexpr int READS = kMxRows / mx_planes(MODE) / TW / 2;  // this warp's reads
+    static constexpr int REGS = (READS * TW + 31) / 32;
+    int to[REGS];
+    float factor[REGS];
+
+    // Before the sums are ready: lane l fetches the output rows (-1: none) of the tokens number 32 i + l of this
+    // warp's.
+    __device__ __forceinline__ void fetch(const MxGemm& g, const Tile& ti, int h, int lane) {
+#pragma unroll
+        for (int i = 0; i < REGS; ++i) {
+            const int m = 32 * i + lane, c = (2 * (m / TW) + h) * TW + m % TW;
+            to[i] = -1;
+            factor[i] = 1.0f;
+            if (c < ti.rows) {
+                to[i] = ti.row0 + c;
+                if constexpr (MODE == kMxDigits) factor[i] = g.xf[to[i]];
+                if (g.perm) {
+                    to[i] = __ldg(g.perm + to[i]);
+                    if (to[i] >= g.R) to[i] = -1;
+                }
+            }
+        }
+    }
+
+    // d: the accumulator's first column in this warp's lanes; n: this lane's output; add: the sums of a part of K.
+    __device__ __forceinline__ void store(const MxGemm& g, const Tile& ti, uint32_t d, int h, int n, bool add) const {
+#pragma unroll
+        for (int j = 0; j < READS; ++j) {
+            const int c0 = (2 * j + h) * TW;
+            if (c0 >= ti.rows) break;
+            uint32_t v[CW], lo[CW];
+            tmem_ld16(d + (MODE == kMxDigits ? 8 : 1) * c0, v);
+            if constexpr (PARTS) tmem_ld16(d + mx_pad16(ti.rows) + c0, lo);
+            tmem_wait_ld();
+#pragma unroll
+            for (int i = 0; i < TW; ++i) {
+                const int m = j * TW + i;
+                const int row = __shfl_sync(kFull, to[m / 32], m % 32);
+                float f = __uint_as_float(v[i]);
+                if constexpr (PARTS) f += __uint_as_float(lo[i]);
+                if constexpr (MODE == kMxDigits) {  // small digits first
+                    const uint32_t* w = v + 8 * i;
+                    f = ((__uint_as_float(w[0]) + __uint_as_float(w[1])) +
+                         ((__uint_as_float(w[2]) + __uint_as_float(w[3])) +
+                          ((__uint_as_float(w[4]) + __uint_as_float(w[5])) +
+                           (__uint_as_float(w[6]) + __uint_as_float(w[7]))))) *
+                        __shfl_sync(kFull, factor[m / 32], m % 32);
+                }
+                float* const y = g.y + (long long)row * g.N + n;
+                if (row >= 0 && n < g.N) {
+                    if (add) atomicAdd(y, f);
+                    else *y = f;
+                }
+            }
+        }
+    }
+};
+
+}  // namespace
+}  // namespace ql

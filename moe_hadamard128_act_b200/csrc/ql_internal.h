@@ -46,6 +46,9 @@ cudaError_t make_tmap_2d(const void* base, long long rows, long long width_bytes
 // [box_y rows][128 codes], each 16 codes spread over 16 bytes of shared memory (8 of them used), 128-byte swizzle.
 cudaError_t make_tmap_u4_spread(const void* base, long long rows, long long K, int box_y, CUtensorMap* out);
 
+// The same over rows of 512 bytes (scale blocks), box [box_y][512 bytes], no swizzle.
+cudaError_t make_tmap_blocks(const void* base, long long rows, int box_y, CUtensorMap* out);
+
 // Per-device facts, cached on first use.
 struct DeviceInfo {
     int sm_count;
@@ -249,7 +252,7 @@ constexpr int kMxTopk = 64;    // pairs of a token at most
 // What the host decides for a product over R rows: the mode, the tokens of a block at most, scale blocks per 128
 // columns of a slot, and whether tiles may be cut along K between two CTAs (y is then zeroed by the quantiser).
 struct MxPlan {
-    int mode, nt, nblk, split;
+    int mode, nt, nblk, split, pair;  // pair: two CTAs to a tile (launch_mx_pair)
 };
 MxPlan mx_plan(bool a16, int R, int N, int K, int E, int sms);
 inline long long mx_slots(int R, int E, int nt) { return E ? (long long)R / nt + E + 1 : ((long long)R + nt - 1) / nt; }
@@ -285,6 +288,7 @@ struct MxGemm {
     MxPlan plan;
 };
 cudaError_t launch_mx_gemm(const MxGemm& g, cudaStream_t s);
+cudaError_t launch_mx_pair(const MxGemm& g, cudaStream_t s);  // modes kMxA4 and kMxParts
 
 // ---- launch trace (ql_trace_enable / ql_trace_read) --------------------------------------
 // trace_begin records a start event for one library launch when tracing is on

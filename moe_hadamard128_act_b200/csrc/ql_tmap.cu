@@ -1,6 +1,6 @@
 // ql_tmap.cu -- host-side construction of TMA tensor maps for 2-D matrices of
-// bytes (packed weights, int8 activations) or of 4-bit codes that the copy
-// spreads to bytes, cached by (address, shape, box, swizzle, element) since the
+// bytes (packed weights, int8 activations), of 4-bit codes that the copy
+// spreads to bytes or of scale blocks, cached by (address, shape, box, swizzle, element) since the
 // same weight is encoded again on every call.
 #include <mutex>
 
@@ -74,6 +74,10 @@ cudaError_t make_tmap_2d(const void* base, long long rows, long long width_bytes
 cudaError_t make_tmap_u4_spread(const void* base, long long rows, long long K, int box_y, CUtensorMap* out) {
     return make_tmap(base, CU_TENSOR_MAP_DATA_TYPE_16U4_ALIGN16B, rows, K, K / 2, 128, box_y,
                      CU_TENSOR_MAP_SWIZZLE_128B, out);
+}
+
+cudaError_t make_tmap_blocks(const void* base, long long rows, int box_y, CUtensorMap* out) {
+    return make_tmap(base, CU_TENSOR_MAP_DATA_TYPE_INT32, rows, 128, 512, 128, box_y, CU_TENSOR_MAP_SWIZZLE_NONE, out);
 }
 
 }  // namespace ql
