@@ -63,7 +63,8 @@ __global__ void __launch_bounds__(kWarps * 32) k_mx_quant(const T* W, int N, int
 // Activations into the order of the product's tiles (mx_layout.cuh).  A CTA takes 128-column units of one row
 // of x, quantised once and written to every place that the row has among the sorted rows: its own (offsets
 // null, or sorted rows given), or one for each of the token's topk pairs, at the pair's position inv[] in its
-// expert's segment.
+// expert's segment.  Up to kMxFusedPairs pairs come without a permutation: every CTA counts its pairs' places
+// from the ids, and pairs with an id outside [0, E) are flagged and their outputs zeroed here.
 struct Place {
     uint8_t *codes, *scale, *low;  // where the row's codes, its scales and its low part's scales begin
     float* y;                      // its output
@@ -98,10 +99,36 @@ __global__ void __launch_bounds__(kWarps * 32) k_mx_act(const MxAct a) {
     __shared__ Place places[kMxTopk];
     const int G = a.K / 128, x = blockIdx.x, nt = a.plan.nt, nblk = a.plan.nblk;
     const int dests = a.ids ? a.topk : 1;
+    const int lane = threadIdx.x & 15;
+    const __nv_bfloat16* const xr = a.x + (long long)x * a.K;
+    int g0 = (blockIdx.y * kWarps + (threadIdx.x >> 5)) * 2;
+    float v[8];  // the next unit's values: on their way while the places are worked out
+    auto load = [&]() { load8(xr + min(g0 + (int)((threadIdx.x >> 4) & 1), G - 1) * 128 + 8 * lane, v); };
+    load();
     for (int j = threadIdx.x >> 5; j < dests; j += kWarps) {
         const long long y = a.ids ? (long long)x * a.topk + j : x;
         int r = x, e = 0, first = 0, end = a.R;
-        if (a.ids) {
+        if (a.ids && !a.inv) {  // few pairs: the pair's place among all, by counting
+            e = __ldg(a.ids + y);
+            r = 0;
+            int size = 0;
+            for (int i = threadIdx.x & 31; i < a.R; i += 32) {
+                const int o = __ldg(a.ids + i);
+                first += o >= 0 && o < e;
+                size += o == e;
+                r += o == e && i < y;
+            }
+            first = __reduce_add_sync(kFull, first);
+            end = first + __reduce_add_sync(kFull, size);
+            r = first + __reduce_add_sync(kFull, r);
+            if (e < 0 || e >= a.E) {
+                r = -1;
+                if (blockIdx.y == 0) {
+                    for (int n = threadIdx.x & 31; n < a.N; n += 32) a.y[y * a.N + n] = 0.0f;
+                    if ((threadIdx.x & 31) == 0) atomicOr(a.err, (unsigned)QL_DEVERR_EXPERT_ID);
+                }
+            }
+        } else if (a.ids) {
             r = __ldg(a.inv + y);
             e = __ldg(a.ids + y);
             if (e < 0 || e >= a.E || r < 0 || r >= a.R) r = -1;
@@ -132,35 +159,37 @@ __global__ void __launch_bounds__(kWarps * 32) k_mx_act(const MxAct a) {
             for (int n = blockIdx.y * blockDim.x + threadIdx.x; n < a.N; n += gridDim.y * blockDim.x) y[n] = 0.0f;
         }
     }
-    const int lane = threadIdx.x & 15;
-    const __nv_bfloat16* const xr = a.x + (long long)x * a.K;
-    for (int g0 = (blockIdx.y * kWarps + (threadIdx.x >> 5)) * 2; g0 < G; g0 += gridDim.y * kWarps * 2) {
+    while (g0 < G) {
         const int g = g0 + ((threadIdx.x >> 4) & 1);
-        float v[8];
-        load8(xr + min(g, G - 1) * 128 + 8 * lane, v);
+        const bool first_unit = g0 == 0;
+        float w[8];
+#pragma unroll
+        for (int k = 0; k < 8; ++k) w[k] = v[k];
+        g0 += gridDim.y * kWarps * 2;
+        if (g0 < G) load();  // the next unit's values are on their way while this one is worked on
         if (a.rotate) {
-            mx_fwht128(v, lane);
+            mx_fwht128(w, lane);
             if constexpr (MODE != kMxA4) {
 #pragma unroll
-                for (int k = 0; k < 8; ++k) v[k] = __bfloat162float(__float2bfloat16_rn(v[k]));
+                for (int k = 0; k < 8; ++k) w[k] = __bfloat162float(__float2bfloat16_rn(w[k]));
             }
         }
         uint32_t byte, c = 0, d[8];
         uint2 hi, lo;
         if constexpr (MODE == kMxA4) {
-            c = mx_quant8(v, byte);
+            c = mx_quant8(w, byte);
         } else if constexpr (MODE == kMxParts) {
-            mx_split8(v, hi, lo, byte);
+            mx_split8(w, hi, lo, byte);
         } else {
-            const uint32_t m = mx_block_max(v);
+            const uint32_t m = mx_block_max(w);
             // Blocks of ordinary size settle that the row is not a small one; zeros fit any factor.  The row's
             // first block answers for the row, whatever it holds.
             int up = 0;
-            if (__any_sync(kFull, m < kSmallRow && (m || g0 == 0))) up = row_up(xr, G, a.rotate);
-            if (g0 == 0 && (threadIdx.x & 31) == 0)
+            if (__any_sync(kFull, m < kSmallRow && (m || first_unit))) up = row_up(xr, G, a.rotate);
+            if (first_unit && (threadIdx.x & 31) == 0)
                 for (int j = 0; j < dests; ++j)
                     if (places[j].row >= 0) a.factors[places[j].row] = up ? 0x1p-32f : 1.0f;
-            mx_digits8(v, m >> 23, up, d, byte);
+            mx_digits8(w, m >> 23, up, d, byte);
         }
         const uint32_t word = mx_scale_word(byte, lane);
         const uint32_t lword = MODE == kMxParts ? mx_scale_word(byte == 255 ? 255u : byte - 5u, lane) : 0u;
@@ -168,8 +197,8 @@ __global__ void __launch_bounds__(kWarps * 32) k_mx_act(const MxAct a) {
         if constexpr (MODE == kMxDigits) {
 #pragma unroll
             for (int k = 0; k < 4; ++k) {
-                const uint32_t w = (word >> (8 * k)) & 0xFFu;
-                dword |= (w == 255 ? 255u : w - 3u * (lane & 7)) << (8 * k);
+                const uint32_t b = (word >> (8 * k)) & 0xFFu;
+                dword |= (b == 255 ? 255u : b - 3u * (lane & 7)) << (8 * k);
             }
         }
         if (g >= G) continue;

@@ -49,6 +49,7 @@
 namespace ql {
 namespace {
 
+constexpr int kFirst = 8;  // weight steps ahead of the activations (12, 6, 4: 0.1 to 0.7 us slower at 1 row)
 constexpr int B_FULL = 0, B_EMPTY = kMaxStages, B_ACCF = 2 * kMaxStages, B_ACCE = B_ACCF + 2, B_DRAIN = B_ACCE + 2,
               NBARS = B_DRAIN + 1;
 
@@ -87,7 +88,7 @@ __global__ void __launch_bounds__(kThreads, 1) k_mx_gemm(const __grid_constant__
     extern __shared__ uint8_t smem_raw[];
     __shared__ __align__(8) uint64_t bars[NBARS];
     __shared__ uint32_t tmem_slot;
-    __shared__ int cum[1025];
+    __shared__ Routing rt;
     constexpr bool PARTS = MODE == kMxParts;
     constexpr int KBS = PARTS ? 1 : 2;  // 128-column blocks per step
     const MxGemm& g = p.g;
@@ -132,10 +133,10 @@ __global__ void __launch_bounds__(kThreads, 1) k_mx_gemm(const __grid_constant__
             asm volatile("fence.mbarrier_init.release.cluster;\n" ::: "memory");
         }
         __syncwarp();
-        if (!g.offsets) {  // one weight: its stream starts at once
-            Tiles<TM> first(g, cum, KS, blockIdx.x, gridDim.x, g.plan.split);
+        if (!grouped(g)) {  // one weight: its stream starts at once
+            Tiles<TM> first(g, rt, KS, blockIdx.x, gridDim.x, g.plan.split);
             if (first.next(ti)) {
-                ahead = min(p.stages, ti.k1 - ti.k0);
+                ahead = min(kFirst, min(p.stages, ti.k1 - ti.k0));
                 for (int k = 0; k < ahead; ++k) load_weights(ti, ti.k0 + k, k, leader);
             }
         }
@@ -144,12 +145,12 @@ __global__ void __launch_bounds__(kThreads, 1) k_mx_gemm(const __grid_constant__
                      "r"(kTmemCols));
         asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;\n");
     }
-    if (g.offsets) count_blocks(g, cum, warp, lane);
+    if (grouped(g)) route(g, rt, warp, lane);
     fence_before();
     __syncthreads();
     fence_after();
     const uint32_t tmem = (uint32_t)uniform((int)tmem_slot);
-    Tiles<TM> tiles(g, cum, KS, blockIdx.x, gridDim.x, g.plan.split);
+    Tiles<TM> tiles(g, rt, KS, blockIdx.x, gridDim.x, g.plan.split);
 
     // The three issuing roles run as whole warps, with every operand the same in all lanes, and one elected lane
     // issues: the instructions take their operands from uniform registers, which a lone lane's values would have
@@ -162,6 +163,9 @@ __global__ void __launch_bounds__(kThreads, 1) k_mx_gemm(const __grid_constant__
             ti.wb = uniform(ti.wb);
             for (int k = uniform(ti.k0), k1 = uniform(ti.k1); k < k1; ++k, ++step) {
                 if (step >= ahead) {
+                    // The first steps' weights are enough until the activations are there, whose copies would
+                    // queue behind any more.
+                    if (step == ahead) asm volatile("griddepcontrol.wait;\n" ::: "memory");
                     if (!__all_sync(kFull, mbar_wait(bar(B_EMPTY + s), ph, lim))) {
                         dead = true;
                         break;
@@ -268,7 +272,7 @@ __global__ void __launch_bounds__(kThreads, 1) k_mx_gemm(const __grid_constant__
         while (tiles.next(ti)) {
             const int b = tl & 1;
             Epilogue<MODE> epi;
-            epi.fetch(g, ti, h, lane);
+            epi.fetch(g, rt, ti, h, lane);
             if (!__all_sync(kFull, mbar_wait(bar(B_ACCF + b), (tl >> 1) & 1, lim))) {  // together
                 dead = true;
                 break;
@@ -306,7 +310,7 @@ cudaError_t run(const MxGemm& g, cudaStream_t s) {
     p.acc_cols = (int)align_up(rows, 32);
     p.sf0 = 2 * p.acc_cols;
     p.sf_cols = KBS * 4 * (1 + nblk);
-    if (di.smem_optin < (size_t)kSmemMax + 8 * 1024) return cudaErrorInvalidValue;
+    if (di.smem_optin < (size_t)kSmemMax + 12 * 1024) return cudaErrorInvalidValue;
     p.stages = (kSmemMax - 1024) / p.stage_bytes;
     if (p.stages > ((int)kTmemCols - p.sf0) / p.sf_cols) p.stages = ((int)kTmemCols - p.sf0) / p.sf_cols;
     if (p.stages > kMaxStages) p.stages = kMaxStages;
@@ -327,7 +331,7 @@ cudaError_t run(const MxGemm& g, cudaStream_t s) {
         if (e != cudaSuccess) return e;
         if (dev < 64) attr_set[dev] = true;
     }
-    const long long tiles = (long long)((g.N + TM - 1) / TM) * mx_slots(g.R, g.offsets ? g.E : 0, g.plan.nt);
+    const long long tiles = (long long)((g.N + TM - 1) / TM) * mx_slots(g.R, g.offsets || g.ids ? g.E : 0, g.plan.nt);
     const long long ctas = (g.plan.split ? 2 : 1) * tiles;
     cudaLaunchConfig_t cfg = {};
     cfg.gridDim = dim3((unsigned)(ctas < di.sm_count ? ctas : di.sm_count));

@@ -121,7 +121,7 @@ __global__ void __launch_bounds__(kThreads, 1) k_mx_pair(const __grid_constant__
     extern __shared__ uint8_t smem_raw[];
     __shared__ __align__(8) uint64_t bars[NBARS];
     __shared__ uint32_t tmem_slot;
-    __shared__ int cum[1025];
+    __shared__ Routing rt;
     constexpr bool PARTS = MODE == kMxParts;
     constexpr int KBC = PARTS ? 1 : 2;  // 128-column blocks per 128-byte column
     constexpr int KBS = KBC * SUB;      // and per step
@@ -158,13 +158,13 @@ __global__ void __launch_bounds__(kThreads, 1) k_mx_pair(const __grid_constant__
                      "r"(kTmemCols));
         asm volatile("tcgen05.relinquish_alloc_permit.cta_group::2.sync.aligned;\n");
     }
-    if (g.offsets) count_blocks(g, cum, warp, lane);
+    if (grouped(g)) route(g, rt, warp, lane);
     fence_before();
     __syncthreads();
     cluster_sync();  // the other CTA's barriers are there
     fence_after();
     const uint32_t tmem = (uint32_t)uniform((int)tmem_slot);
-    Tiles<PM> tiles(g, cum, KS, blockIdx.x >> 1, gridDim.x >> 1, false);
+    Tiles<PM> tiles(g, rt, KS, blockIdx.x >> 1, gridDim.x >> 1, false);
 
     if (warp == 0) {  // ---- weights and their scales ----
         const bool leader = elect();
@@ -183,10 +183,10 @@ __global__ void __launch_bounds__(kThreads, 1) k_mx_pair(const __grid_constant__
                 const uint32_t slot = base + s * p.stage_bytes, fb = in_even(bar(B_FULL + s));
                 if (leader) {
                     // spread copies count the packed bytes; what lies past the last column or block counts too
+                    const int subs = min(SUB, (G - k * KBS + KBC - 1) / KBC);  // fewer in the last step
                     if (rank == 0)
-                        mbar_expect_tx(bar(B_FULL + s), 2 * (SUB * (PARTS ? A_BYTES / 2 : A_BYTES) + KBS * 512));
-#pragma unroll
-                    for (int u = 0; u < SUB; ++u)
+                        mbar_expect_tx(bar(B_FULL + s), 2 * (subs * (PARTS ? A_BYTES / 2 : A_BYTES) + KBS * 512));
+                    for (int u = 0; u < subs; ++u)
                         pair_load_2d(slot + u * A_BYTES, &p.tmW, (k * SUB + u) * 128, row, fb);
                     pair_load_2d(slot + sa_off, &p.tmSW, 0, sf + k * KBS, fb);
                 }
@@ -210,9 +210,9 @@ __global__ void __launch_bounds__(kThreads, 1) k_mx_pair(const __grid_constant__
                 }
                 const uint32_t slot = base + s * p.stage_bytes, fb = in_even(bar(B_FULL + s));
                 if (leader) {
-                    if (rank == 0) mbar_expect_tx(bar(B_FULL + s), 2 * (SUB * half * 128 + KBS * nblk * 512));
-#pragma unroll
-                    for (int u = 0; u < SUB; ++u) {
+                    const int subs = min(SUB, (G - k * KBS + KBC - 1) / KBC);
+                    if (rank == 0) mbar_expect_tx(bar(B_FULL + s), 2 * (subs * half * 128 + KBS * nblk * 512));
+                    for (int u = 0; u < subs; ++u) {
                         const int x = (k * SUB + u) * 128;
                         const uint32_t dst = slot + b_off + u * b_col;
                         int r = 0;
@@ -319,7 +319,7 @@ __global__ void __launch_bounds__(kThreads, 1) k_mx_pair(const __grid_constant__
         while (tiles.next(ti)) {
             const int b = tl & 1;
             Epilogue<MODE> epi;
-            epi.fetch(g, ti, h, lane);
+            epi.fetch(g, rt, ti, h, lane);
             if (!__all_sync(kFull, mbar_wait(bar(B_ACCF + b), (tl >> 1) & 1, lim))) {  // together
                 dead = true;
                 break;
@@ -356,7 +356,7 @@ cudaError_t run(const MxGemm& g, cudaStream_t s) {
     DeviceInfo di;
     cudaError_t e = device_info(&di);
     if (e != cudaSuccess) return e;
-    if (di.smem_optin < (size_t)kSmemMax + 8 * 1024) return cudaErrorInvalidValue;
+    if (di.smem_optin < (size_t)kSmemMax + 12 * 1024) return cudaErrorInvalidValue;
     constexpr bool PARTS = MODE == kMxParts;
     constexpr int P = mx_planes(MODE), KBS = (PARTS ? 1 : 2) * SUB;
     PairParams p;
@@ -374,7 +374,7 @@ cudaError_t run(const MxGemm& g, cudaStream_t s) {
     if (p.stages < 2 || p.sf_slots < 2) return cudaErrorInvalidValue;
     const long long wrows = (long long)g.E * g.N, xrows = (long long)P * g.R, xbytes = PARTS ? g.K : g.K / 2;
     const long long G = g.K / 128, wblocks = (long long)g.E * ((g.N + TM - 1) / TM) * G;
-    const long long xblocks = mx_slots(g.R, g.offsets ? g.E : 0, g.plan.nt) * G * nblk;
+    const long long xblocks = mx_slots(g.R, g.offsets || g.ids ? g.E : 0, g.plan.nt) * G * nblk;
     e = PARTS ? make_tmap_u4_spread(g.codes, wrows, g.K, TM, &p.tmW)
               : make_tmap_2d(g.codes, wrows, g.K / 2, g.K / 2, 128, TM, CU_TENSOR_MAP_SWIZZLE_128B, &p.tmW);
     if (e == cudaSuccess) e = make_tmap_2d(g.xq, xrows, xbytes, xbytes, 128, SMALL, CU_TENSOR_MAP_SWIZZLE_128B, &p.tmX);
@@ -408,7 +408,7 @@ cudaError_t run(const MxGemm& g, cudaStream_t s) {
         if (pairs < 1) return cudaErrorInvalidValue;
         if (dev < 64) pairs_of[dev] = pairs;
     }
-    const long long tiles = (long long)((g.N + PM - 1) / PM) * mx_slots(g.R, g.offsets ? g.E : 0, g.plan.nt);
+    const long long tiles = (long long)((g.N + PM - 1) / PM) * mx_slots(g.R, g.offsets || g.ids ? g.E : 0, g.plan.nt);
     cfg.gridDim = dim3((unsigned)(2 * (tiles < pairs ? tiles : pairs)));
     cfg.numAttrs = 2;
     e = cudaLaunchKernelEx(&cfg, k_mx_pair<MODE>, p);

@@ -16,7 +16,7 @@ constexpr int kEpiWarp0 = 4, kEpiWarps = 8;
 constexpr int kThreads = 32 * (kEpiWarp0 + kEpiWarps);
 constexpr uint32_t kTmemCols = 512;
 constexpr int CW = 16;  // accumulator columns per tensor-memory read
-constexpr int kSmemMax = 219 * 1024;  // dynamic shared memory of a CTA at most
+constexpr int kSmemMax = 215 * 1024;  // dynamic shared memory of a CTA at most
 
 __device__ __forceinline__ uint64_t desc_sw128(uint32_t addr) {
     // K-major, 128-byte swizzle: 8-row atoms 1024 bytes apart (SBO), version 1.
@@ -67,18 +67,34 @@ struct Tile {
     int k0, k1;  // its steps
 };
 
+// What the CTA knows of the experts' segments.
+struct Routing {
+    int cum[1025];             // token blocks of the experts before e
+    int offsets[1025];         // of ids: the segments,
+    int perm[kMxFusedPairs];   // and the pairs in sorted order
+    int ids[kMxFusedPairs];
+};
+__device__ __forceinline__ bool grouped(const MxGemm& g) { return g.offsets || g.ids; }
+__device__ __forceinline__ void segment(const MxGemm& g, const Routing& rt, int e, int& a, int& b) {
+    if (g.ids) {
+        a = rt.offsets[e];
+        b = rt.offsets[e + 1];
+    } else {
+        mx_segment(g.offsets, e, g.R, a, b);
+    }
+}
+
 // The tiles of unit `id` of `units` (a CTA, or a pair of them), each role walking the same list: weight block (of
-// TR rows) by weight block within an expert so that its token blocks share the weights in L2; cum[e]: token blocks
-// of the experts before e.  With `split` tiles may be cut along K between two units.
+// TR rows) by weight block within an expert so that its token blocks share the weights in L2.  With `split` tiles may be cut along K between two units.
 template <int TR>
 struct Tiles {
     const MxGemm& g;
-    const int* cum;
+    const Routing& rt;
     int NB, KS, units, total, t;
     long long u, end;  // split: the unit's run of steps
-    __device__ Tiles(const MxGemm& g_, const int* cum_, int KS_, int id, int units_, bool split)
-        : g(g_), cum(cum_), NB((g_.N + TR - 1) / TR), KS(KS_), units(units_), t(id), u(-1), end(0) {
-        total = NB * (g.offsets ? cum[g.E] : (g.R + g.plan.nt - 1) / g.plan.nt);
+    __device__ Tiles(const MxGemm& g_, const Routing& rt_, int KS_, int id, int units_, bool split)
+        : g(g_), rt(rt_), NB((g_.N + TR - 1) / TR), KS(KS_), units(units_), t(id), u(-1), end(0) {
+        total = NB * (grouped(g) ? rt.cum[g.E] : (g.R + g.plan.nt - 1) / g.plan.nt);
         // Runs of whole tiles lose up to a tile's time in the last round; past eight rounds that is little.
         if (split && (2 * total <= units || (total > units && total < 8 * units && total % units))) {
             const int parts = 2 * total <= units ? 2 * total : units;
@@ -102,18 +118,18 @@ struct Tiles {
             t += units;
         }
         int e = 0, i, first = 0, count = g.R;
-        if (g.offsets) {
+        if (grouped(g)) {
             int hi = g.E;  // the largest e with cum[e] * NB <= tile
             while (hi - e > 1) {
                 const int m = (e + hi) >> 1;
-                if (cum[m] * NB <= tile) e = m;
+                if (rt.cum[m] * NB <= tile) e = m;
                 else hi = m;
             }
-            const int nb = cum[e + 1] - cum[e], local = tile - cum[e] * NB;
+            const int nb = rt.cum[e + 1] - rt.cum[e], local = tile - rt.cum[e] * NB;
             o.wb = local / nb;
             i = local - o.wb * nb;
             int last;
-            mx_segment(g.offsets, e, g.R, first, last);
+            segment(g, rt, e, first, last);
             count = last - first;
         } else {
             const int nb = (g.R + g.plan.nt - 1) / g.plan.nt;
@@ -128,13 +144,41 @@ struct Tiles {
     }
 };
 
-// Token blocks of each expert, then their exclusive sums: cum[e], e <= E.  By the whole CTA; the sums are there
-// after the caller's next barrier.
-__device__ __forceinline__ void count_blocks(const MxGemm& g, int* cum, int warp, int lane) {
-    for (int e = threadIdx.x; e < g.E; e += kThreads) {
-        int a, b;
-        if (!mx_segment(g.offsets, e, g.R, a, b)) atomicOr(g.err, (unsigned)QL_DEVERR_BOUNDS);
-        cum[e] = (b - a + g.plan.nt - 1) / g.plan.nt;
+// Token blocks of each expert, then their exclusive sums: cum[e], e <= E; of ids, the segments and the sorted order
+// first (stable: by expert, then by pair).  By the whole CTA; the sums are there after the caller's next barrier.
+__device__ __forceinline__ void route(const MxGemm& g, Routing& rt, int warp, int lane) {
+    int* const cum = rt.cum;
+    if (g.ids) {
+        // ids in shared memory, 128 of them with the missing ones out of range; each thread counts for its experts,
+        // then for its pair.
+        if (threadIdx.x < kMxFusedPairs) {
+            const int e = threadIdx.x < g.R ? __ldg(g.ids + threadIdx.x) : -1;
+            rt.ids[threadIdx.x] = e >= 0 && e < g.E ? e : g.E;
+        }
+        __syncthreads();
+        for (int e = threadIdx.x; e <= g.E; e += kThreads) {
+            int below = 0, size = 0;
+#pragma unroll 8
+            for (int i = 0; i < kMxFusedPairs; ++i) {
+                below += rt.ids[i] < e;
+                size += rt.ids[i] == e;
+            }
+            rt.offsets[e] = below;
+            if (e < g.E) cum[e] = (size + g.plan.nt - 1) / g.plan.nt;
+        }
+        if (threadIdx.x < g.R) {
+            const int p = threadIdx.x, e = rt.ids[p];
+            int r = 0;
+#pragma unroll 8
+            for (int i = 0; i < kMxFusedPairs; ++i) r += rt.ids[i] < e || (rt.ids[i] == e && i < p);
+            if (e < g.E) rt.perm[r] = p;
+        }
+    } else {
+        for (int e = threadIdx.x; e < g.E; e += kThreads) {
+            int a, b;
+            if (!mx_segment(g.offsets, e, g.R, a, b)) atomicOr(g.err, (unsigned)QL_DEVERR_BOUNDS);
+            cum[e] = (b - a + g.plan.nt - 1) / g.plan.nt;
+        }
     }
     __syncthreads();
     if (warp != 3) return;
@@ -166,7 +210,7 @@ struct Epilogue {
 
     // Before the sums are ready: lane l fetches the output rows (-1: none) of the tokens number 32 i + l of this
     // warp's.
-    __device__ __forceinline__ void fetch(const MxGemm& g, const Tile& ti, int h, int lane) {
+    __device__ __forceinline__ void fetch(const MxGemm& g, const Routing& rt, const Tile& ti, int h, int lane) {
 #pragma unroll
         for (int i = 0; i < REGS; ++i) {
             const int m = 32 * i + lane, c = (2 * (m / TW) + h) * TW + m % TW;
@@ -175,7 +219,9 @@ struct Epilogue {
             if (c < ti.rows) {
                 to[i] = ti.row0 + c;
                 if constexpr (MODE == kMxDigits) factor[i] = g.xf[to[i]];
-                if (g.perm) {
+                if (g.ids) {
+                    to[i] = rt.perm[to[i]];
+                } else if (g.perm) {
                     to[i] = __ldg(g.perm + to[i]);
                     if (to[i] >= g.R) to[i] = -1;
                 }

@@ -192,14 +192,14 @@ int mx_product(const void* x, const void* codes, const void* scales, int flags, 
                const int32_t* offsets, const int32_t* perm, const int32_t* ids, int topk, const MxWs& w, uint8_t* ws,
                float* y, unsigned* err, cudaStream_t s) {
     MxAct q{static_cast<const __nv_bfloat16*>(x), R, K, (flags & QL_HADAMARD) ? 1 : 0, w.plan, offsets, E, ids,
-            ids ? reinterpret_cast<const int32_t*>(ws + w.inv) : nullptr, topk, ws + w.xq, ws + w.xs,
-            reinterpret_cast<float*>(ws + w.xf), y, N};
+            perm ? reinterpret_cast<const int32_t*>(ws + w.inv) : nullptr, topk, ws + w.xq, ws + w.xs,
+            reinterpret_cast<float*>(ws + w.xf), y, N, err};
     int t = trace_begin(QL_KIND_ACT_QUANT, s);
     cudaError_t e = launch_mx_act(q, s);
     trace_end(t, s);
     if (e != cudaSuccess) return from_cuda(e);
     MxGemm g{static_cast<const uint8_t*>(codes), static_cast<const uint8_t*>(scales), q.codes, q.scales, q.factors,
-             offsets, perm, y, err, R, E ? E : 1, N, K, w.plan};
+             offsets, perm, offsets ? nullptr : ids, y, err, R, E ? E : 1, N, K, w.plan};
     t = trace_begin(E ? QL_KIND_MOE_GEMM : QL_KIND_MX_GEMM, s);
     e = launch_mx_gemm(g, s);
     trace_end(t, s);
@@ -725,6 +725,9 @@ int moe_gate_up(const void* x, const int32_t* topk_ids, const float* topk_weight
         int32_t* const counts = reinterpret_cast<int32_t*>(b + w.counts);
         int32_t* const offsets = reinterpret_cast<int32_t*>(b + w.offsets);
         int32_t* const perm = reinterpret_cast<int32_t*>(b + w.perm);
+        if (R <= kMxFusedPairs)  // few pairs: the kernels work the places out themselves
+            return mx_product(x, experts->codes, experts->scales, experts->flags, R, experts->N, experts->K,
+                              experts->E, nullptr, nullptr, topk_ids, topk, w, b, y, di.err_word, s);
         MoePermuteOut po;
         po.inv = reinterpret_cast<int32_t*>(b + w.inv);
         po.yz = y;  // rows of pairs with a bad expert id are zeroed

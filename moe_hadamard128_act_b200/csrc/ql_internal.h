@@ -258,7 +258,8 @@ MxPlan mx_plan(bool a16, int R, int N, int K, int E, int sms);
 inline long long mx_slots(int R, int E, int nt) { return E ? (long long)R / nt + E + 1 : ((long long)R + nt - 1) / nt; }
 // The product's activations: R sorted rows.  Rows of x are sorted rows themselves (ids null; offsets [E + 1] null:
 // one expert owns all), or tokens whose topk pairs, of experts ids[t * topk + j], sit at sorted rows
-// inv[t * topk + j].
+// inv[t * topk + j]; for up to kMxFusedPairs pairs inv is null and both kernels work the places out from the ids.
+constexpr int kMxFusedPairs = 128;
 struct MxAct {
     const __nv_bfloat16* x;
     int R, K, rotate;
@@ -272,6 +273,7 @@ struct MxAct {
     float* factors;   // digits: what each sorted row's sums are to be multiplied by
     float* y;         // plan.split: the rows' outputs, zeroed here
     int N;
+    unsigned* err;
 };
 cudaError_t launch_mx_act(const MxAct& a, cudaStream_t s);
 struct MxGemm {
@@ -282,6 +284,7 @@ struct MxGemm {
     const float* xf;
     const int32_t* offsets;  // null: one expert owns every row
     const int32_t* perm;     // row r goes to y row perm[r]; null: to row r
+    const int32_t* ids;      // few pairs: their experts, in place of offsets and perm
     float* y;                // [R][N]
     unsigned* err;
     int R, E, N, K;
