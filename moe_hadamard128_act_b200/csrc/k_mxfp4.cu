@@ -14,6 +14,8 @@ namespace ql {
 namespace {
 
 constexpr int kWarps = 8;
+// Warps of the activations' kernel (4 and 2: up to 3 and 6 us slower at 2048 rows).
+constexpr int kActWarps = 8;
 
 __device__ __forceinline__ void load8(const float* p, float v[8]) {
     const float4 a = __ldg(reinterpret_cast<const float4*>(p)), b = __ldg(reinterpret_cast<const float4*>(p) + 1);
@@ -91,7 +93,7 @@ __device__ __noinline__ int row_up(const __nv_bfloat16* x, int G, int rotate) {
 }
 
 template <int MODE>
-__global__ void __launch_bounds__(kWarps * 32) k_mx_act(const MxAct a) {
+__global__ void __launch_bounds__(kActWarps * 32) k_mx_act(const MxAct a) {
     // Launched while the kernel before it ends: nothing is read or written before that one is done, and only then
     // may the product start its weight stream, which waits for nothing else.
     asm volatile("griddepcontrol.wait;\n" ::: "memory");
@@ -101,11 +103,11 @@ __global__ void __launch_bounds__(kWarps * 32) k_mx_act(const MxAct a) {
     const int dests = a.ids ? a.topk : 1;
     const int lane = threadIdx.x & 15;
     const __nv_bfloat16* const xr = a.x + (long long)x * a.K;
-    int g0 = (blockIdx.y * kWarps + (threadIdx.x >> 5)) * 2;
+    int g0 = (blockIdx.y * kActWarps + (threadIdx.x >> 5)) * 2;
     float v[8];  // the next unit's values: on their way while the places are worked out
     auto load = [&]() { load8(xr + min(g0 + (int)((threadIdx.x >> 4) & 1), G - 1) * 128 + 8 * lane, v); };
     load();
-    for (int j = threadIdx.x >> 5; j < dests; j += kWarps) {
+    for (int j = threadIdx.x >> 5; j < dests; j += kActWarps) {
         const long long y = a.ids ? (long long)x * a.topk + j : x;
         int r = x, e = 0, first = 0, end = a.R;
         if (a.ids && !a.inv) {  // few pairs: the pair's place among all, by counting
@@ -165,7 +167,7 @@ __global__ void __launch_bounds__(kWarps * 32) k_mx_act(const MxAct a) {
         float w[8];
 #pragma unroll
         for (int k = 0; k < 8; ++k) w[k] = v[k];
-        g0 += gridDim.y * kWarps * 2;
+        g0 += gridDim.y * kActWarps * 2;
         if (g0 < G) load();  // the next unit's values are on their way while this one is worked on
         if (a.rotate) {
             mx_fwht128(w, lane);
@@ -304,11 +306,11 @@ cudaError_t launch_mx_quant_rows(const void* x, int M, int K, int rotate, uint8_
 
 cudaError_t launch_mx_act(const MxAct& a, cudaStream_t s) {
     // One CTA a row; few rows are cut along K instead, so that their columns are not walked one after another.
-    const int rows = a.ids ? a.R / a.topk : a.R, passes = (a.K / 128 + 2 * kWarps - 1) / (2 * kWarps);
+    const int rows = a.ids ? a.R / a.topk : a.R, passes = (a.K / 128 + 2 * kActWarps - 1) / (2 * kActWarps);
     const dim3 grid((unsigned)rows, (unsigned)(rows < 148 ? passes : 1));
     cudaLaunchConfig_t cfg = {};
     cfg.gridDim = grid;
-    cfg.blockDim = dim3(kWarps * 32);
+    cfg.blockDim = dim3(kActWarps * 32);
     cfg.stream = s;
     cudaLaunchAttribute attr[1];
     attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;

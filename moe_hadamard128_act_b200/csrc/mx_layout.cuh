@@ -54,12 +54,23 @@ __device__ __forceinline__ int mx_warp_search(int E, int v, Key key) {
     return base + 31 - __clz(m | 1u);
 }
 
-// Two fp32 values to E2M1 by the hardware conversion (round to nearest even, saturating to +-6): the low
-// nibble holds `lo`, the high nibble `hi`.
-__device__ __forceinline__ uint32_t cvt_e2m1x2(float hi, float lo) {
+// Eight fp32 values to E2M1 by the hardware conversion (round to nearest even, saturating to +-6), the first in
+// the low nibble.
+__device__ __forceinline__ uint32_t cvt_e2m1x8(const float v[8]) {
     uint32_t r;
-    asm("{\n .reg .b8 t;\n cvt.rn.satfinite.e2m1x2.f32 t, %1, %2;\n cvt.u32.u8 %0, t;\n}\n" : "=r"(r) : "f"(hi), "f"(lo));
+    asm("{\n .reg .b8 a, b, c, d;\n"
+        " cvt.rn.satfinite.e2m1x2.f32 a, %2, %1;\n cvt.rn.satfinite.e2m1x2.f32 b, %4, %3;\n"
+        " cvt.rn.satfinite.e2m1x2.f32 c, %6, %5;\n cvt.rn.satfinite.e2m1x2.f32 d, %8, %7;\n"
+        " mov.b32 %0, {a, b, c, d};\n}\n"
+        : "=r"(r)
+        : "f"(v[0]), "f"(v[1]), "f"(v[2]), "f"(v[3]), "f"(v[4]), "f"(v[5]), "f"(v[6]), "f"(v[7]));
     return r;
+}
+// Largest magnitude of three, a NaN if there is one.
+__device__ __forceinline__ float max3_abs(float a, float b, float c) {
+    float d;
+    asm("max.NaN.abs.f32 %0, %1, %2, %3;\n" : "=f"(d) : "f"(a), "f"(b), "f"(c));
+    return d;
 }
 // Two E2M1 codes (low byte of c) to f16x2, exact.
 __device__ __forceinline__ uint32_t e2m1x2_to_f16x2(uint32_t c) {
@@ -102,9 +113,8 @@ __device__ __forceinline__ void mx_fwht128(float v[8], int lane) {
 // A 32-block's largest magnitude (4 lanes) as fp32 bits without the sign: unsigned order puts infinities and
 // NaN (exponent field 255) above every finite value.
 __device__ __forceinline__ uint32_t mx_block_max(const float v[8]) {
-    uint32_t m = 0;
-#pragma unroll
-    for (int i = 0; i < 8; ++i) m = max(m, __float_as_uint(v[i]) & 0x7FFFFFFFu);
+    const float a = max3_abs(max3_abs(max3_abs(v[0], v[1], v[2]), v[3], v[4]), v[5], v[6]);
+    uint32_t m = __float_as_uint(max3_abs(a, v[7], v[7]));
     m = max(m, __shfl_xor_sync(kFull, m, 1));
     return max(m, __shfl_xor_sync(kFull, m, 2));
 }
@@ -122,9 +132,10 @@ __device__ __forceinline__ uint32_t mx_quant8(const float v[8], uint32_t& byte) 
     const uint32_t ex = mx_block_max(v) >> 23;
     byte = ex > 2 ? ex - 2 : 0;
     const float inv = __uint_as_float((254u - byte) << 23);
-    uint32_t c = 0;
+    float s[8];
 #pragma unroll
-    for (int i = 0; i < 4; ++i) c |= cvt_e2m1x2(v[2 * i + 1] * inv, v[2 * i] * inv) << (8 * i);
+    for (int i = 0; i < 8; ++i) s[i] = v[i] * inv;
+    uint32_t c = cvt_e2m1x8(s);
     if (ex == 255) {  // an infinity or a NaN
         byte = 255;
         c = 0;
@@ -133,31 +144,43 @@ __device__ __forceinline__ uint32_t mx_quant8(const float v[8], uint32_t& byte) 
 }
 
 // A 32-block of bf16 values as eight E2M1 digits, v = 2^e sum_p d_p 8^-p: e puts the block's largest magnitude
-// into [2, 4), each digit is what is left rounded to E2M1 (off by at most 0.5 below 4), and eight times the
-// remainder, at most 4 again, goes to the next.  Every step is exact in fp32; after the eighth at most
-// 0.5 * 8^-7 of 2^e is left, 2^-23 of the largest magnitude, and nothing of values down to 2^-16 of it.
+// into [1, 2), v / 2^e is rounded to a multiple of 8^-7, and that number's digits in base 8 from -4 to 3 are all
+// E2M1 values.  So v is off by at most 2^-22 of the largest magnitude, and not at all down to 2^-15 of it.
 // byte: the first digit's scale; digit p's is byte - 3 p, so it is held at 21 or more: a block below 2^-105
 // loses its last digits, unless its whole row is small and was scaled up by 2^up (see k_mx_act).
+// The digits are taken in integers: 4 in every digit makes them 0 .. 7, three bits each, which are spread to
+// nibbles; a byte permute then looks four of them up at once, and two more rounds of permutes turn one
+// value's digits into one digit's values (digit p of the lane's eight values: d[p], low nibble first).
 __device__ __forceinline__ void mx_digits8(const float v[8], uint32_t ex, int up, uint32_t d[8], uint32_t& byte) {
-    byte = (uint32_t)max((int)ex - 1 + up, 21);
-    // 2^-e has the exponent field f; past 254 as a product of two powers (with up only).
+    byte = (uint32_t)max((int)ex + up, 21);
+    // 2^-e has the exponent field f; past 254 as a product of two powers (with up only).  Then 8^7 = 2^21.
     const int f = 254 - ((int)byte - up);
-    const float i0 = __uint_as_float((uint32_t)min(f, 254) << 23), i1 = __uint_as_float((uint32_t)(127 + max(f - 254, 0)) << 23);
-    float r[8];
+    const float i0 = __uint_as_float((uint32_t)min(f, 254) << 23);
+    const float i1 = __uint_as_float((uint32_t)(127 + 21 + max(f - 254, 0)) << 23);
+    constexpr uint32_t kLow = 0x0A0C0D0Eu, kHigh = 0x05040200u;  // E2M1 of -4 .. -1 and 0 .. 3
+    uint32_t lo[4], hi[4];  // values 2 j and 2 j + 1 in a byte; digits 7 .. 4 and 3 .. 0 from the low byte up
 #pragma unroll
-    for (int i = 0; i < 8; ++i) r[i] = v[i] * i0 * i1;
-#pragma unroll
-    for (int p = 0; p < 8; ++p) {
-        d[p] = 0;
-#pragma unroll
-        for (int i = 0; i < 4; ++i) {
-            const uint32_t c = cvt_e2m1x2(r[2 * i + 1], r[2 * i]);
-            d[p] |= c << (8 * i);
-            const uint32_t h = e2m1x2_to_f16x2(c);
-            r[2 * i] = (r[2 * i] - f16_bits_to_float((uint16_t)h)) * 8.0f;
-            r[2 * i + 1] = (r[2 * i + 1] - f16_bits_to_float((uint16_t)(h >> 16))) * 8.0f;
-        }
+    for (int i = 0; i < 8; ++i) {
+        uint32_t u = (uint32_t)(__float2int_rn(v[i] * i0 * i1) + 0x924924);
+        // Fields moved up by multiply-adds (u + 15 f is u with its field f shifted by 4), which the integer pipe,
+        // the busiest one here, does not see.
+        u += (u & 0xFFF000u) * 15u;
+        u += (u & 0x0FC00FC0u) * 3u;
+        u += u & 0x38383838u;
+        const uint32_t l = __byte_perm(kLow, kHigh, u & 0xFFFFu), h = __byte_perm(kLow, kHigh, u >> 16);
+        lo[i >> 1] = (i & 1) ? lo[i >> 1] + l * 16u : l;
+        hi[i >> 1] = (i & 1) ? hi[i >> 1] + h * 16u : h;
     }
+    auto turn = [](const uint32_t a[4], uint32_t& b0, uint32_t& b1, uint32_t& b2, uint32_t& b3) {
+        const uint32_t p = __byte_perm(a[0], a[1], 0x5140), q = __byte_perm(a[2], a[3], 0x5140);  // bytes 0 and 1
+        const uint32_t r = __byte_perm(a[0], a[1], 0x7362), t = __byte_perm(a[2], a[3], 0x7362);  // bytes 2 and 3
+        b0 = __byte_perm(p, q, 0x5410);
+        b1 = __byte_perm(p, q, 0x7632);
+        b2 = __byte_perm(r, t, 0x5410);
+        b3 = __byte_perm(r, t, 0x7632);
+    };
+    turn(lo, d[7], d[6], d[5], d[4]);
+    turn(hi, d[3], d[2], d[1], d[0]);
     if (ex == 255) {  // an infinity or a NaN
         byte = 255;
 #pragma unroll
