@@ -2,10 +2,11 @@
 // weights and activations, the packer of given codes, and the values that
 // packed codes stand for.
 //
-// Half a warp takes one row's 128 columns, 8 neighbouring values a lane (one
-// 16-byte load of bf16): the rotation's shuffles stay inside the half warp, a
-// 32-block is 4 lanes, and the 128 columns' four scale bytes are one word of
-// the scale layout (mx_layout.cuh).  Bound by HBM: 2 (bf16) or 4 (fp32) bytes in
+// Eight lanes take one row's 128 columns, 16 neighbouring values a lane (one
+// 32-byte load of bf16): the rotation's shuffles stay inside the eight, a
+// 32-block is 2 lanes, and the 128 columns' four scale bytes are one word of
+// the scale layout (mx_layout.cuh).  With half as many values a lane the work
+// around the values, not the memory, set the time.  Bound by HBM: 2 (bf16) or 4 (fp32) bytes in
 // and 17/32 byte out per value.
 #include "mx_layout.cuh"
 #include "ql_internal.h"
@@ -14,48 +15,77 @@ namespace ql {
 namespace {
 
 constexpr int kWarps = 8;
-// Warps of the activations' kernel (4 and 2: up to 3 and 6 us slower at 2048 rows).
-constexpr int kActWarps = 8;
+// Warps of the activations' kernel (8: 1 to 2 us slower from 1600 rows on, with the last pass half empty).
+constexpr int kActWarps = 4;
 
-__device__ __forceinline__ void load8(const float* p, float v[8]) {
-    const float4 a = __ldg(reinterpret_cast<const float4*>(p)), b = __ldg(reinterpret_cast<const float4*>(p) + 1);
-    v[0] = a.x; v[1] = a.y; v[2] = a.z; v[3] = a.w;
-    v[4] = b.x; v[5] = b.y; v[6] = b.z; v[7] = b.w;
-}
-__device__ __forceinline__ void load8(const __nv_bfloat16* p, float v[8]) {
-    const uint4 r = __ldg(reinterpret_cast<const uint4*>(p));
-    const uint32_t w[4] = {r.x, r.y, r.z, r.w};
-#pragma unroll
-    for (int i = 0; i < 4; ++i) {
-        v[2 * i] = __uint_as_float(w[i] << 16);
-        v[2 * i + 1] = __uint_as_float(w[i] & 0xFFFF0000u);
+// 32 bytes, read once; one load if the tensor is 32-byte aligned (rows are whole multiples of that), else two.
+__device__ __forceinline__ void ldg32(const void* p, bool wide, uint32_t w[8]) {
+    if (wide) {
+        asm volatile("ld.global.nc.L1::no_allocate.v8.b32 {%0,%1,%2,%3,%4,%5,%6,%7}, [%8];\n"
+                     : "=r"(w[0]), "=r"(w[1]), "=r"(w[2]), "=r"(w[3]), "=r"(w[4]), "=r"(w[5]), "=r"(w[6]), "=r"(w[7])
+                     : "l"(p));
+    } else {
+        const uint4 a = __ldg(static_cast<const uint4*>(p)), b = __ldg(static_cast<const uint4*>(p) + 1);
+        w[0] = a.x; w[1] = a.y; w[2] = a.z; w[3] = a.w;
+        w[4] = b.x; w[5] = b.y; w[6] = b.z; w[7] = b.w;
     }
 }
+__device__ __forceinline__ bool aligned32(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 31u) == 0; }
+// A lane's 16 values as they are loaded, and in fp32.
+template <typename T>
+struct Raw;
+template <>
+struct Raw<float> {
+    uint32_t w[16];
+    __device__ __forceinline__ void load(const float* p, bool wide) {
+        ldg32(p, wide, w);
+        ldg32(p + 8, wide, w + 8);
+    }
+    __device__ __forceinline__ void get(float v[16]) const {
+#pragma unroll
+        for (int i = 0; i < 16; ++i) v[i] = __uint_as_float(w[i]);
+    }
+};
+template <>
+struct Raw<__nv_bfloat16> {
+    uint32_t w[8];
+    __device__ __forceinline__ void load(const __nv_bfloat16* p, bool wide) { ldg32(p, wide, w); }
+    __device__ __forceinline__ void get(float v[16]) const {
+#pragma unroll
+        for (int i = 0; i < 8; ++i) {
+            v[2 * i] = __uint_as_float(w[i] << 16);
+            v[2 * i + 1] = __uint_as_float(w[i] & 0xFFFF0000u);
+        }
+    }
+};
 
 // Rows [0, N) of W to packed MXFP4; rows up to the next multiple of 128 get zero scales.  A CTA takes kRows
-// rows and walks them 128 columns a half warp at a time, all rows' loads of a column first.
-constexpr int kRows = 4;
+// rows and walks them 128 columns to eight lanes, all rows' loads of a column first.
+constexpr int kRows = 2;  // 4: registers halve the warps, pack 121 us against 103 at 21504 x 5376
 template <typename T>
 __global__ void __launch_bounds__(kWarps * 32) k_mx_quant(const T* W, int N, int K, int rotate, uint8_t* codes,
                                                           uint8_t* scales) {
-    const int lane = threadIdx.x & 15, G = K / 128;
+    const int lane = threadIdx.x & 7, G = K / 128;
+    const bool wide = aligned32(W);
     const int r0 = blockIdx.x * kRows;
-    // every lane of a warp goes through the same iterations (the shuffles want both halves)
-    for (int g0 = (blockIdx.y * kWarps + (threadIdx.x >> 5)) * 2; g0 < G; g0 += gridDim.y * kWarps * 2) {
-        const int g = g0 + ((threadIdx.x >> 4) & 1);
+    // every lane of a warp goes through the same iterations (the shuffles want all of them)
+    for (int g0 = (blockIdx.y * kWarps + (threadIdx.x >> 5)) * 4; g0 < G; g0 += gridDim.y * kWarps * 4) {
+        const int g = g0 + ((threadIdx.x >> 3) & 3);
         const int gl = min(g, G - 1);
-        float v[kRows][8];
+        Raw<T> raw[kRows];
 #pragma unroll
-        for (int i = 0; i < kRows; ++i) load8(W + (long long)min(r0 + i, N - 1) * K + gl * 128 + 8 * lane, v[i]);
+        for (int i = 0; i < kRows; ++i) raw[i].load(W + (long long)min(r0 + i, N - 1) * K + gl * 128 + 16 * lane, wide);
 #pragma unroll
         for (int i = 0; i < kRows; ++i) {
             const int r = r0 + i;
-            if (rotate) mx_fwht128(v[i], lane);
+            float v[16];
+            raw[i].get(v);
+            if (rotate) mx_fwht128(v, lane);
             uint32_t byte;
-            const uint32_t c = mx_quant8(v[i], byte);
+            const uint2 c = mx_quant16(v, byte);
             uint32_t word = mx_scale_word(byte, lane);
             if (g >= G) continue;
-            if (r < N) *reinterpret_cast<uint32_t*>(codes + (long long)r * (K / 2) + g * 64 + 4 * lane) = c;
+            if (r < N) *reinterpret_cast<uint2*>(codes + (long long)r * (K / 2) + g * 64 + 8 * lane) = c;
             else word = 0;
             if (lane == 0) *reinterpret_cast<uint32_t*>(scales + mx_scale_at(r >> 7, G, g, 1, r & 127)) = word;
         }
@@ -78,16 +108,16 @@ struct Place {
 // block below 2^-105; beside a value of 2^-64 that is at most 2^-65 of it, and without one the row is moved up.
 constexpr uint32_t kSmallRow = 63u << 23;  // 2^-64
 __device__ __noinline__ int row_up(const __nv_bfloat16* x, int G, int rotate) {
-    const int lane = threadIdx.x & 15;
+    const int lane = threadIdx.x & 7;
     uint32_t m = 0;
-    for (int g0 = 0; g0 < G; g0 += 2) {
-        float v[8];
-        load8(x + min(g0 + (int)((threadIdx.x >> 4) & 1), G - 1) * 128 + 8 * lane, v);
+    for (int g0 = 0; g0 < G; g0 += 4) {
+        Raw<__nv_bfloat16> raw;
+        raw.load(x + min(g0 + (int)((threadIdx.x >> 3) & 3), G - 1) * 128 + 16 * lane, aligned32(x));
+        float v[16];
+        raw.get(v);
         if (rotate) mx_fwht128(v, lane);
 #pragma unroll
-        for (int i = 0; i < 8; ++i) v[i] = __bfloat162float(__float2bfloat16_rn(v[i]));
-#pragma unroll
-        for (int i = 0; i < 8; ++i) m = max(m, __float_as_uint(v[i]) & 0x7FFFFFFFu);
+        for (int i = 0; i < 16; ++i) m = max(m, __float_as_uint(__bfloat162float(__float2bfloat16_rn(v[i]))) & 0x7FFFFFFFu);
     }
     return __reduce_max_sync(kFull, m) < kSmallRow ? 32 : 0;
 }
@@ -101,11 +131,12 @@ __global__ void __launch_bounds__(kActWarps * 32) k_mx_act(const MxAct a) {
     __shared__ Place places[kMxTopk];
     const int G = a.K / 128, x = blockIdx.x, nt = a.plan.nt, nblk = a.plan.nblk;
     const int dests = a.ids ? a.topk : 1;
-    const int lane = threadIdx.x & 15;
+    const int lane = threadIdx.x & 7;
     const __nv_bfloat16* const xr = a.x + (long long)x * a.K;
-    int g0 = (blockIdx.y * kActWarps + (threadIdx.x >> 5)) * 2;
-    float v[8];  // the next unit's values: on their way while the places are worked out
-    auto load = [&]() { load8(xr + min(g0 + (int)((threadIdx.x >> 4) & 1), G - 1) * 128 + 8 * lane, v); };
+    const bool wide = aligned32(a.x);
+    int g0 = (blockIdx.y * kActWarps + (threadIdx.x >> 5)) * 4;
+    Raw<__nv_bfloat16> raw;  // the next unit's values: on their way while the places are worked out
+    auto load = [&]() { raw.load(xr + min(g0 + (int)((threadIdx.x >> 3) & 3), G - 1) * 128 + 16 * lane, wide); };
     load();
     for (int j = threadIdx.x >> 5; j < dests; j += kActWarps) {
         const long long y = a.ids ? (long long)x * a.topk + j : x;
@@ -162,28 +193,28 @@ __global__ void __launch_bounds__(kActWarps * 32) k_mx_act(const MxAct a) {
         }
     }
     while (g0 < G) {
-        const int g = g0 + ((threadIdx.x >> 4) & 1);
+        const int g = g0 + ((threadIdx.x >> 3) & 3);
         const bool first_unit = g0 == 0;
-        float w[8];
-#pragma unroll
-        for (int k = 0; k < 8; ++k) w[k] = v[k];
-        g0 += gridDim.y * kActWarps * 2;
+        float v[16];
+        raw.get(v);
+        g0 += gridDim.y * kActWarps * 4;
         if (g0 < G) load();  // the next unit's values are on their way while this one is worked on
         if (a.rotate) {
-            mx_fwht128(w, lane);
+            mx_fwht128(v, lane);
             if constexpr (MODE != kMxA4) {
 #pragma unroll
-                for (int k = 0; k < 8; ++k) w[k] = __bfloat162float(__float2bfloat16_rn(w[k]));
+                for (int k = 0; k < 16; ++k) v[k] = __bfloat162float(__float2bfloat16_rn(v[k]));
             }
         }
-        uint32_t byte, c = 0, d[8];
-        uint2 hi, lo;
+        uint32_t byte, d0[8], d1[8];
+        uint2 c;
+        uint4 hi, lo;
         if constexpr (MODE == kMxA4) {
-            c = mx_quant8(w, byte);
+            c = mx_quant16(v, byte);
         } else if constexpr (MODE == kMxParts) {
-            mx_split8(w, hi, lo, byte);
+            mx_split16(v, hi, lo, byte);
         } else {
-            const uint32_t m = mx_block_max(w);
+            const uint32_t m = mx_block_max(v);
             // Blocks of ordinary size settle that the row is not a small one; zeros fit any factor.  The row's
             // first block answers for the row, whatever it holds.
             int up = 0;
@@ -191,16 +222,18 @@ __global__ void __launch_bounds__(kActWarps * 32) k_mx_act(const MxAct a) {
             if (first_unit && (threadIdx.x & 31) == 0)
                 for (int j = 0; j < dests; ++j)
                     if (places[j].row >= 0) a.factors[places[j].row] = up ? 0x1p-32f : 1.0f;
-            mx_digits8(w, m >> 23, up, d, byte);
+            byte = mx_digits_byte(m >> 23, up);
+            mx_digits8(v, byte, up, d0);
+            mx_digits8(v + 8, byte, up, d1);
         }
         const uint32_t word = mx_scale_word(byte, lane);
         const uint32_t lword = MODE == kMxParts ? mx_scale_word(byte == 255 ? 255u : byte - 5u, lane) : 0u;
-        uint32_t dword = 0;  // digits: lane p < 8 holds digit p's four scales, each 3 p below the first's
+        uint32_t dword = 0;  // digits: lane p holds digit p's four scales, each 3 p below the first's
         if constexpr (MODE == kMxDigits) {
 #pragma unroll
             for (int k = 0; k < 4; ++k) {
                 const uint32_t b = (word >> (8 * k)) & 0xFFu;
-                dword |= (b == 255 ? 255u : b - 3u * (lane & 7)) << (8 * k);
+                dword |= (b == 255 ? 255u : b - 3u * lane) << (8 * k);
             }
         }
         if (g >= G) continue;
@@ -209,20 +242,20 @@ __global__ void __launch_bounds__(kActWarps * 32) k_mx_act(const MxAct a) {
             if (p.row < 0) continue;
             const long long sf = (long long)g * nblk * 512;
             if constexpr (MODE == kMxA4) {
-                *reinterpret_cast<uint32_t*>(p.codes + g * 64 + 4 * lane) = c;
+                *reinterpret_cast<uint2*>(p.codes + g * 64 + 8 * lane) = c;
                 if (lane == 0) *reinterpret_cast<uint32_t*>(p.scale + sf) = word;
             } else if constexpr (MODE == kMxParts) {
-                uint8_t* const at = p.codes + g * 128 + 8 * lane;
-                *reinterpret_cast<uint2*>(at) = hi;
-                *reinterpret_cast<uint2*>(at + (long long)a.R * a.K) = lo;
+                uint8_t* const at = p.codes + g * 128 + 16 * lane;
+                *reinterpret_cast<uint4*>(at) = hi;
+                *reinterpret_cast<uint4*>(at + (long long)a.R * a.K) = lo;
                 if (lane == 0) *reinterpret_cast<uint32_t*>(p.scale + sf) = word;
                 if (lane == 1) *reinterpret_cast<uint32_t*>(p.low + sf) = lword;
             } else {
 #pragma unroll
                 for (int k = 0; k < 8; ++k)
-                    *reinterpret_cast<uint32_t*>(p.codes + (long long)k * (a.K / 2) + g * 64 + 4 * lane) = d[k];
-                if (lane < 8)
-                    *reinterpret_cast<uint32_t*>(p.scale + sf + mx_scale_at(0, G, 0, nblk, 8 * p.c + lane)) = dword;
+                    *reinterpret_cast<uint2*>(p.codes + (long long)k * (a.K / 2) + g * 64 + 8 * lane) =
+                        make_uint2(d0[k], d1[k]);
+                *reinterpret_cast<uint32_t*>(p.scale + sf + mx_scale_at(0, G, 0, nblk, 8 * p.c + lane)) = dword;
             }
         }
     }
@@ -287,7 +320,7 @@ __global__ void __launch_bounds__(256) k_mx_dequant(const uint8_t* codes, const 
 
 template <typename T>
 cudaError_t quant(const T* W, int N, int K, int rotate, uint8_t* codes, uint8_t* scales, cudaStream_t s) {
-    const int blocks = (N + 127) / 128 * (128 / kRows), passes = (K / 128 + 2 * kWarps - 1) / (2 * kWarps);
+    const int blocks = (N + 127) / 128 * (128 / kRows), passes = (K / 128 + 4 * kWarps - 1) / (4 * kWarps);
     const dim3 grid((unsigned)blocks, (unsigned)(blocks < 148 ? passes : 1));  // few rows: cut along K too
     k_mx_quant<T><<<grid, kWarps * 32, 0, s>>>(W, N, K, rotate, codes, scales);
     return cudaGetLastError();
@@ -306,7 +339,7 @@ cudaError_t launch_mx_quant_rows(const void* x, int M, int K, int rotate, uint8_
 
 cudaError_t launch_mx_act(const MxAct& a, cudaStream_t s) {
     // One CTA a row; few rows are cut along K instead, so that their columns are not walked one after another.
-    const int rows = a.ids ? a.R / a.topk : a.R, passes = (a.K / 128 + 2 * kActWarps - 1) / (2 * kActWarps);
+    const int rows = a.ids ? a.R / a.topk : a.R, passes = (a.K / 128 + 4 * kActWarps - 1) / (4 * kActWarps);
     const dim3 grid((unsigned)rows, (unsigned)(rows < 148 ? passes : 1));
     cudaLaunchConfig_t cfg = {};
     cfg.gridDim = grid;

@@ -83,62 +83,63 @@ __device__ __forceinline__ float mx_scale(uint32_t b) {
     return __uint_as_float(b == 0 ? 0x00400000u : b == 255 ? 0x7FFFFFFFu : b << 23);
 }
 
-// ---- 128 columns of a row held 8 neighbouring values a lane by 16 lanes (half a warp) -------------------
+// ---- 128 columns of a row held 16 neighbouring values a lane by 8 lanes (a quarter of a warp) -------------
 // The Walsh-Hadamard transform of fwht128_warp, bit for bit: the same butterflies in the same order, strides
-// 1, 2, 4 inside the lane and 8 .. 64 across lanes.
-__device__ __forceinline__ void mx_fwht128(float v[8], int lane) {
+// 1 .. 8 inside the lane and 16 .. 64 across lanes.
+__device__ __forceinline__ void mx_fwht128(float v[16], int lane) {
 #pragma unroll
-    for (int s = 1; s < 8; s <<= 1)
+    for (int s = 1; s < 16; s <<= 1)
 #pragma unroll
-        for (int i = 0; i < 8; ++i)
+        for (int i = 0; i < 16; ++i)
             if (!(i & s)) {
                 const float a = v[i], b = v[i | s];
                 v[i] = __fadd_rn(a, b);
                 v[i | s] = __fsub_rn(a, b);
             }
 #pragma unroll
-    for (int m = 1; m < 16; m <<= 1) {
+    for (int m = 1; m < 8; m <<= 1) {
         const float sgn = (lane & m) ? -1.0f : 1.0f;
 #pragma unroll
-        for (int i = 0; i < 8; ++i) {
+        for (int i = 0; i < 16; ++i) {
             const float o = __shfl_xor_sync(kFull, v[i], m);
             v[i] = __fmaf_rn(sgn, v[i], o);
         }
     }
     const float c = fwht_scale();
 #pragma unroll
-    for (int i = 0; i < 8; ++i) v[i] = __fmul_rn(v[i], c);
+    for (int i = 0; i < 16; ++i) v[i] = __fmul_rn(v[i], c);
 }
 
-// A 32-block's largest magnitude (4 lanes) as fp32 bits without the sign: unsigned order puts infinities and
+// A 32-block's largest magnitude (2 lanes) as fp32 bits without the sign: unsigned order puts infinities and
 // NaN (exponent field 255) above every finite value.
-__device__ __forceinline__ uint32_t mx_block_max(const float v[8]) {
-    const float a = max3_abs(max3_abs(max3_abs(v[0], v[1], v[2]), v[3], v[4]), v[5], v[6]);
-    uint32_t m = __float_as_uint(max3_abs(a, v[7], v[7]));
-    m = max(m, __shfl_xor_sync(kFull, m, 1));
-    return max(m, __shfl_xor_sync(kFull, m, 2));
+__device__ __forceinline__ uint32_t mx_block_max(const float v[16]) {
+    float a = max3_abs(v[0], v[1], v[2]);
+#pragma unroll
+    for (int i = 3; i < 15; i += 2) a = max3_abs(a, v[i], v[i + 1]);
+    const uint32_t m = __float_as_uint(max3_abs(a, v[15], v[15]));
+    return max(m, __shfl_xor_sync(kFull, m, 1));
 }
-// The four blocks' scale bytes as one word, in every lane of the half warp.
+// The four blocks' scale bytes as one word, in all 8 lanes.
 __device__ __forceinline__ uint32_t mx_scale_word(uint32_t byte, int lane) {
-    uint32_t w = byte << (8 * ((lane >> 2) & 3));
-    w |= __shfl_xor_sync(kFull, w, 4);
-    return w | __shfl_xor_sync(kFull, w, 8);
+    uint32_t w = byte << (8 * ((lane >> 1) & 3));
+    w |= __shfl_xor_sync(kFull, w, 2);
+    return w | __shfl_xor_sync(kFull, w, 4);
 }
 
-// MXFP4 of a 32-block: the lane's eight codes (low nibble first) and the scale byte.  floor(log2 amax) is the
+// MXFP4 of a 32-block: the lane's sixteen codes (low nibble first) and the scale byte.  floor(log2 amax) is the
 // exponent field, so the byte e + 127 with e = floor(log2 amax) - 2 is the field less 2, clamped at 0; the
 // division by 2^e is an exact product.
-__device__ __forceinline__ uint32_t mx_quant8(const float v[8], uint32_t& byte) {
+__device__ __forceinline__ uint2 mx_quant16(const float v[16], uint32_t& byte) {
     const uint32_t ex = mx_block_max(v) >> 23;
     byte = ex > 2 ? ex - 2 : 0;
     const float inv = __uint_as_float((254u - byte) << 23);
-    float s[8];
+    float s[16];
 #pragma unroll
-    for (int i = 0; i < 8; ++i) s[i] = v[i] * inv;
-    uint32_t c = cvt_e2m1x8(s);
+    for (int i = 0; i < 16; ++i) s[i] = v[i] * inv;
+    uint2 c = make_uint2(cvt_e2m1x8(s), cvt_e2m1x8(s + 8));
     if (ex == 255) {  // an infinity or a NaN
         byte = 255;
-        c = 0;
+        c = make_uint2(0, 0);
     }
     return c;
 }
@@ -150,9 +151,11 @@ __device__ __forceinline__ uint32_t mx_quant8(const float v[8], uint32_t& byte) 
 // loses its last digits, unless its whole row is small and was scaled up by 2^up (see k_mx_act).
 // The digits are taken in integers: 4 in every digit makes them 0 .. 7, three bits each, which are spread to
 // nibbles; a byte permute then looks four of them up at once, and two more rounds of permutes turn one
-// value's digits into one digit's values (digit p of the lane's eight values: d[p], low nibble first).
-__device__ __forceinline__ void mx_digits8(const float v[8], uint32_t ex, int up, uint32_t d[8], uint32_t& byte) {
-    byte = (uint32_t)max((int)ex + up, 21);
+// value's digits into one digit's values (digit p of eight values: d[p], low nibble first).
+__device__ __forceinline__ uint32_t mx_digits_byte(uint32_t ex, int up) {
+    return ex == 255 ? 255u : (uint32_t)max((int)ex + up, 21);  // 255: an infinity or a NaN
+}
+__device__ __forceinline__ void mx_digits8(const float* v, uint32_t byte, int up, uint32_t d[8]) {
     // 2^-e has the exponent field f; past 254 as a product of two powers (with up only).  Then 8^7 = 2^21.
     const int f = 254 - ((int)byte - up);
     const float i0 = __uint_as_float((uint32_t)min(f, 254) << 23);
@@ -181,8 +184,7 @@ __device__ __forceinline__ void mx_digits8(const float v[8], uint32_t ex, int up
     };
     turn(lo, d[7], d[6], d[5], d[4]);
     turn(hi, d[3], d[2], d[1], d[0]);
-    if (ex == 255) {  // an infinity or a NaN
-        byte = 255;
+    if (byte == 255) {
 #pragma unroll
         for (int p = 0; p < 8; ++p) d[p] = 0;
     }
@@ -193,24 +195,24 @@ __device__ __forceinline__ void mx_digits8(const float v[8], uint32_t ex, int up
 // bf16's eight fits four more, so the sum is exact unless the value is so far below the largest that lo's
 // spacing 2^-9 cuts it: exact from 2^-14 of the largest up, within 2^-22 of it below.  byte: hi's scale; lo's
 // is byte - 5 (e is held at -122 or more for that), or 255 with it.
-__device__ __forceinline__ void mx_split8(const float v[8], uint2& hi, uint2& lo, uint32_t& byte) {
+__device__ __forceinline__ void mx_split16(const float v[16], uint4& hi, uint4& lo, uint32_t& byte) {
     const uint32_t ex = mx_block_max(v) >> 23;
     byte = ex > 12 ? ex - 7 : 5;
     const float inv = __uint_as_float((254u - byte) << 23);
-    uint32_t h[4], l[4];
+    uint32_t h[8], l[8];
 #pragma unroll
-    for (int i = 0; i < 4; ++i) {
+    for (int i = 0; i < 8; ++i) {
         const float a = v[2 * i] * inv, b = v[2 * i + 1] * inv;
         h[i] = cvt_e4m3x2(b, a);
         const uint32_t f = e4m3x2_to_f16x2(h[i]);
         l[i] = cvt_e4m3x2((b - f16_bits_to_float((uint16_t)(f >> 16))) * 32.0f,
                           (a - f16_bits_to_float((uint16_t)f)) * 32.0f);
     }
-    hi = make_uint2(h[0] | h[1] << 16, h[2] | h[3] << 16);
-    lo = make_uint2(l[0] | l[1] << 16, l[2] | l[3] << 16);
+    hi = make_uint4(h[0] | h[1] << 16, h[2] | h[3] << 16, h[4] | h[5] << 16, h[6] | h[7] << 16);
+    lo = make_uint4(l[0] | l[1] << 16, l[2] | l[3] << 16, l[4] | l[5] << 16, l[6] | l[7] << 16);
     if (ex == 255) {  // an infinity or a NaN
         byte = 255;
-        hi = lo = make_uint2(0, 0);
+        hi = lo = make_uint4(0, 0, 0, 0);
     }
 }
 
