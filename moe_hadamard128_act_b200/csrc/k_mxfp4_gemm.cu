@@ -278,11 +278,11 @@ __global__ void __launch_bounds__(kThreads, 1) k_mx_gemm(const __grid_constant__
                 break;
             }
             fence_after();
-            epi.store(g, ti, tmem + b * p.acc_cols + ((uint32_t)(32 * q) << 16), h, ti.wb * TM + 32 * q + lane,
-                      ti.k1 - ti.k0 < KS);
+            epi.drain(ti, tmem + b * p.acc_cols + ((uint32_t)(32 * q) << 16), h);
             fence_before();
             __syncwarp();
             if (lane == 0) arrive(bar(B_ACCE + b));
+            epi.store(g, ti, h, ti.wb * TM + 32 * q + lane, ti.k1 - ti.k0 < KS);
             ++tl;
         }
     }
@@ -357,7 +357,7 @@ MxPlan mx_plan(bool a16, int R, int N, int K, int E, int sms) {
     MxPlan p;
     const long long per = E ? (R + E - 1) / E : R;  // rows an expert
     p.mode = !a16 ? kMxA4 : per <= (E ? 16 : 24) ? kMxDigits : kMxParts;
-    const int P = mx_planes(p.mode), most = kMxRows / P, step = p.mode == kMxDigits ? 2 : 16;
+    const int P = mx_planes(p.mode), most = (p.mode == kMxDigits || E ? kMxRows2 : kMxRows) / P, step = p.mode == kMxDigits ? 2 : 16;
     long long nt = E ? 2 * per : (R + (R + most - 1LL) / most - 1) / ((R + most - 1LL) / most);
     if (nt > most) nt = most;
     p.nt = (int)((nt + step - 1) / step * step);
@@ -365,8 +365,11 @@ MxPlan mx_plan(bool a16, int R, int N, int K, int E, int sms) {
     // Cutting tiles along K costs a zeroed y: worth it while y is small beside the weights.
     const long long tiles = (long long)((N + TM - 1) / TM) * mx_slots(R, 0, p.nt);
     p.split = (long long)R * N * 4 <= (4 << 20) && (E || tiles < 8LL * sms);
-    // Two CTAs to a tile once a token block is wide enough for its operand stream to count.
-    p.pair = p.mode != kMxDigits && p.nt * P >= 64;
+    // Two CTAs to a tile once a token block is wide enough for its operand stream to count: 21504 x 5376 at 64 rows
+    // 20.5 us against 22.3, at 192 rows 27.1 against 30.6.  Experts with 4-bit activations wait for their weights
+    // longer (128 of 1408 x 2816 at 400 tokens 60.8 against 58.9, at 2048 tokens 91.5 against 94); 16-bit parts gain
+    // everywhere (400 tokens 80 against 96).
+    p.pair = p.mode != kMxDigits && p.nt * P >= (E && p.mode == kMxA4 ? kMxRows2 : 64);
     if (p.pair) p.split = 0;
     return p;
 }

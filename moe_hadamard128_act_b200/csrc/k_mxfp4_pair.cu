@@ -17,9 +17,10 @@
 // its commits arrive at the barriers of both.
 // Scale blocks: each CTA brings those of its own weight rows and all of the
 // activations', which the copies to tensor memory put into both CTAs' columns.
-//
-// A step is two of k_mxfp4_gemm.cu's (512 columns of K, or 256): a wait or a commit
-// costs its role about 100 cycles, which shorter steps pay twice as often.
+// Token blocks of up to 192 operand rows have two accumulators, so that an
+// epilogue runs under the next tile's MMAs.  A block of 256, which reads fewer
+// operand bytes a product, fills half of the tensor memory with one: its epilogue
+// takes the sums into registers, gives the accumulator back and then stores.
 //
 // Waits are bounded as in k_mxfp4_gemm.cu; a CTA that gave up stays until copies
 // that it started have landed, and both CTAs leave together.
@@ -29,7 +30,6 @@ namespace ql {
 namespace {
 
 constexpr int PM = 2 * TM;  // weight rows of a pair's tile (MMA M)
-constexpr int SUB = 2;      // 128-byte columns of operands per step
 constexpr int B_FULL = 0, B_EMPTY = kMaxStages, B_ACCF = 2 * kMaxStages, B_ACCE = B_ACCF + 2, B_DRAIN = B_ACCE + 2,
               B_SF = B_DRAIN + 1, NBARS = B_SF + kMaxStages;
 
@@ -38,8 +38,8 @@ struct PairParams {
     CUtensorMap tmX, tmXb;  // activation codes: boxes of 16 and 64 rows x 128 bytes
     CUtensorMap tmSW, tmSX;  // scales as rows of 512 bytes, boxes of a step's blocks
     MxGemm g;
-    int stages, stage_bytes, b_bytes;     // ring; activation codes of a 128-byte column
-    int acc_cols, sf0, sf_cols, sf_slots;  // tensor memory: accumulator stride, scales' first column, columns and slots
+    int stages, stage_bytes;  // ring
+    int nacc, acc_cols, sf0, sf_cols, sf_slots;  // tensor memory: accumulators and their stride, scales' first column, columns and slots
 };
 
 __device__ __forceinline__ uint32_t cluster_rank() {
@@ -123,8 +123,7 @@ __global__ void __launch_bounds__(kThreads, 1) k_mx_pair(const __grid_constant__
     __shared__ uint32_t tmem_slot;
     __shared__ Routing rt;
     constexpr bool PARTS = MODE == kMxParts;
-    constexpr int KBC = PARTS ? 1 : 2;  // 128-column blocks per 128-byte column
-    constexpr int KBS = KBC * SUB;      // and per step
+    constexpr int KBS = PARTS ? 1 : 2;  // 128-column blocks per step
     const MxGemm& g = p.g;
     const uint32_t base = (smem_u32(smem_raw) + 1023u) & ~1023u;
     auto bar = [&](int i) { return smem_u32(&bars[i]); };
@@ -132,9 +131,9 @@ __global__ void __launch_bounds__(kThreads, 1) k_mx_pair(const __grid_constant__
     const int rank = (int)cluster_rank();
     const int G = g.K / 128, KS = (G + KBS - 1) / KBS, NB = (g.N + TM - 1) / TM;
     const int nblk = g.plan.nblk;
-    // A slot: weight codes, this CTA's half of the activation codes (each SUB 128-byte columns), weight scales (KBS
-    // blocks), activation scales (KBS x nblk blocks).
-    const int b_off = SUB * A_BYTES, b_col = p.b_bytes, sa_off = p.stage_bytes - KBS * (1 + nblk) * 512, sb_off = sa_off + KBS * 512;
+    // A slot: weight codes, this CTA's half of the activation codes, weight scales (KBS blocks), activation scales
+    // (KBS x nblk blocks).
+    const int b_off = A_BYTES, sa_off = p.stage_bytes - KBS * (1 + nblk) * 512, sb_off = sa_off + KBS * 512;
 
     asm volatile("griddepcontrol.launch_dependents;\n" ::: "memory");  // the next call's quantiser may stand by
     const unsigned long long lim = wait_limit(g.err);
@@ -183,11 +182,8 @@ __global__ void __launch_bounds__(kThreads, 1) k_mx_pair(const __grid_constant__
                 const uint32_t slot = base + s * p.stage_bytes, fb = in_even(bar(B_FULL + s));
                 if (leader) {
                     // spread copies count the packed bytes; what lies past the last column or block counts too
-                    const int subs = min(SUB, (G - k * KBS + KBC - 1) / KBC);  // fewer in the last step
-                    if (rank == 0)
-                        mbar_expect_tx(bar(B_FULL + s), 2 * (subs * (PARTS ? A_BYTES / 2 : A_BYTES) + KBS * 512));
-                    for (int u = 0; u < subs; ++u)
-                        pair_load_2d(slot + u * A_BYTES, &p.tmW, (k * SUB + u) * 128, row, fb);
+                    if (rank == 0) mbar_expect_tx(bar(B_FULL + s), 2 * ((PARTS ? A_BYTES / 2 : A_BYTES) + KBS * 512));
+                    pair_load_2d(slot, &p.tmW, k * 128, row, fb);
                     pair_load_2d(slot + sa_off, &p.tmSW, 0, sf + k * KBS, fb);
                 }
                 __syncwarp();
@@ -210,15 +206,11 @@ __global__ void __launch_bounds__(kThreads, 1) k_mx_pair(const __grid_constant__
                 }
                 const uint32_t slot = base + s * p.stage_bytes, fb = in_even(bar(B_FULL + s));
                 if (leader) {
-                    const int subs = min(SUB, (G - k * KBS + KBC - 1) / KBC);
-                    if (rank == 0) mbar_expect_tx(bar(B_FULL + s), 2 * (subs * half * 128 + KBS * nblk * 512));
-                    for (int u = 0; u < subs; ++u) {
-                        const int x = (k * SUB + u) * 128;
-                        const uint32_t dst = slot + b_off + u * b_col;
-                        int r = 0;
-                        for (; r + BIG <= half; r += BIG) pair_load_2d(dst + r * 128, &p.tmXb, x, row + r, fb);
-                        for (; r < half; r += SMALL) pair_load_2d(dst + r * 128, &p.tmX, x, row + r, fb);
-                    }
+                    if (rank == 0) mbar_expect_tx(bar(B_FULL + s), 2 * (half * 128 + KBS * nblk * 512));
+                    int r = 0;
+                    for (; r + BIG <= half; r += BIG)
+                        pair_load_2d(slot + b_off + r * 128, &p.tmXb, k * 128, row + r, fb);
+                    for (; r < half; r += SMALL) pair_load_2d(slot + b_off + r * 128, &p.tmX, k * 128, row + r, fb);
                     pair_load_2d(slot + sb_off, &p.tmSX, 0, sf + k * KBS * nblk, fb);
                 }
                 __syncwarp();
@@ -233,7 +225,9 @@ __global__ void __launch_bounds__(kThreads, 1) k_mx_pair(const __grid_constant__
         while (!dead && tiles.next(ti)) {
             for (int k = 0; k < KS; ++k, ++step) {
                 bool ok = pair_wait(bar(B_FULL + s), ph, lim);
-                if (step >= p.sf_slots) {  // the MMAs that read these columns are done
+                // The MMAs that read these columns before are done: the load that filled the slot waited for them
+                // if there are as many columns as slots.
+                if (p.sf_slots < p.stages && step >= p.sf_slots) {
                     ok = ok && mbar_wait(bar(B_EMPTY + os), oph, lim);
                     if (++os == p.stages) { os = 0; oph ^= 1; }
                 }
@@ -267,8 +261,8 @@ __global__ void __launch_bounds__(kThreads, 1) k_mx_pair(const __grid_constant__
         const bool leader = elect();
         int s = 0, q = 0, qph = 0, tl = 0;
         while (!dead && tiles.next(ti)) {
-            const int b = tl & 1;
-            if (!__all_sync(kFull, pair_wait(bar(B_ACCE + b), ((tl >> 1) & 1) ^ 1, lim))) {  // both epilogues are done
+            const int b = p.nacc == 2 ? tl & 1 : 0, use = p.nacc == 2 ? tl >> 1 : tl;
+            if (!__all_sync(kFull, pair_wait(bar(B_ACCE + b), (use & 1) ^ 1, lim))) {  // both epilogues are done
                 dead = true;
                 break;
             }
@@ -287,16 +281,12 @@ __global__ void __launch_bounds__(kThreads, 1) k_mx_pair(const __grid_constant__
                 const uint64_t ad = desc_sw128(slot), bd = desc_sw128(slot + b_off);
                 if (leader) {
 #pragma unroll
-                    for (int u = 0; u < SUB; ++u)
-#pragma unroll
-                        for (int j = 0; j < 4; ++j) {  // 32 bytes of every row: +2 in the descriptors' address field
-                            // its scales' block and byte
-                            const int i = u * KBC + (PARTS ? 0 : j >> 1), byte = PARTS ? j : 2 * (j & 1);
-                            if (i < kbs)
-                                pair_mma<MODE>(d, ad + u * (A_BYTES >> 4) + 2 * j, bd + u * (b_col >> 4) + 2 * j,
-                                               id0 | (uint32_t)byte << 4 | (uint32_t)byte << 29, sf + 4 * i,
-                                               sfb + 4 * nblk * i, (k | u | j) ? 1u : 0u);
-                        }
+                    for (int j = 0; j < 4; ++j) {  // 32 bytes of every row: +2 in the descriptors' address field
+                        const int i = PARTS ? 0 : j >> 1, byte = PARTS ? j : 2 * (j & 1);  // its scales' block and byte
+                        if (i < kbs)
+                            pair_mma<MODE>(d, ad + 2 * j, bd + 2 * j, id0 | (uint32_t)byte << 4 | (uint32_t)byte << 29,
+                                           sf + 4 * i, sfb + 4 * nblk * i, (k | j) ? 1u : 0u);
+                    }
                     pair_commit(bar(B_EMPTY + s));  // both CTAs' slots may be refilled once these are done
                 }
                 __syncwarp();
@@ -317,19 +307,19 @@ __global__ void __launch_bounds__(kThreads, 1) k_mx_pair(const __grid_constant__
         asm volatile("griddepcontrol.wait;\n" ::: "memory");
         int tl = 0;
         while (tiles.next(ti)) {
-            const int b = tl & 1;
+            const int b = p.nacc == 2 ? tl & 1 : 0, use = p.nacc == 2 ? tl >> 1 : tl;
             Epilogue<MODE> epi;
             epi.fetch(g, rt, ti, h, lane);
-            if (!__all_sync(kFull, mbar_wait(bar(B_ACCF + b), (tl >> 1) & 1, lim))) {  // together
+            if (!__all_sync(kFull, mbar_wait(bar(B_ACCF + b), use & 1, lim))) {  // together
                 dead = true;
                 break;
             }
             fence_after();
-            epi.store(g, ti, tmem + b * p.acc_cols + ((uint32_t)(32 * q) << 16), h,
-                      (2 * ti.wb + rank) * TM + 32 * q + lane, false);
+            epi.drain(ti, tmem + b * p.acc_cols + ((uint32_t)(32 * q) << 16), h);
             fence_before();
             __syncwarp();
             if (lane == 0) pair_arrive(in_even(bar(B_ACCE + b)));
+            epi.store(g, ti, h, (2 * ti.wb + rank) * TM + 32 * q + lane, false);
             ++tl;
         }
     }
@@ -358,14 +348,14 @@ cudaError_t run(const MxGemm& g, cudaStream_t s) {
     if (e != cudaSuccess) return e;
     if (di.smem_optin < (size_t)kSmemMax + 12 * 1024) return cudaErrorInvalidValue;
     constexpr bool PARTS = MODE == kMxParts;
-    constexpr int P = mx_planes(MODE), KBS = (PARTS ? 1 : 2) * SUB;
+    constexpr int P = mx_planes(MODE), KBS = PARTS ? 1 : 2;
     PairParams p;
     p.g = g;
     const int nblk = g.plan.nblk, rows = (P * g.plan.nt + 31) / 32 * 32;  // operand rows of a full token block
-    p.b_bytes = (int)align_up(rows / 2 * 128, 1024);
-    p.stage_bytes = (int)align_up(SUB * (A_BYTES + p.b_bytes) + KBS * (1 + nblk) * 512, 1024);
+    p.stage_bytes = (int)align_up(A_BYTES + rows / 2 * 128 + KBS * (1 + nblk) * 512, 1024);
     p.acc_cols = rows;
-    p.sf0 = 2 * p.acc_cols;
+    p.nacc = rows <= kMxRows2 ? 2 : 1;
+    p.sf0 = p.nacc * p.acc_cols;
     p.sf_cols = KBS * 4 * (1 + nblk);
     p.stages = (kSmemMax - 1024) / p.stage_bytes;
     if (p.stages > kMaxStages) p.stages = kMaxStages;

@@ -203,7 +203,8 @@ template <int MODE>
 struct Epilogue {
     static constexpr bool PARTS = MODE == kMxParts;
     static constexpr int TW = MODE == kMxDigits ? CW / 8 : CW;        // tokens of a tensor-memory read
-    static constexpr int READS = kMxRows / mx_planes(MODE) / TW / 2;  // this warp's reads
+    // this warp's reads (16-bit activations: a block has no more than kMxRows2 operand rows in digits)
+    static constexpr int READS = (MODE == kMxDigits ? kMxRows2 : kMxRows) / mx_planes(MODE) / TW / 2;
     static constexpr int REGS = (READS * TW + 31) / 32;
     int to[REGS];
     float factor[REGS];
@@ -229,34 +230,56 @@ struct Epilogue {
         }
     }
 
-    // d: the accumulator's first column in this warp's lanes; n: this lane's output; add: the sums of a part of K.
-    __device__ __forceinline__ void store(const MxGemm& g, const Tile& ti, uint32_t d, int h, int n, bool add) const {
+    // This warp's sums of the accumulator whose first column in its lanes is d, as bits: sum[j][i] is that of its
+    // token number TW j + i.  The accumulator is free once every warp has returned.
+    uint32_t sum[READS][TW];
+    __device__ __forceinline__ void drain(const Tile& ti, uint32_t d, int h) {
+        const int n16 = mx_pad16(ti.rows);
 #pragma unroll
         for (int j = 0; j < READS; ++j) {
             const int c0 = (2 * j + h) * TW;
             if (c0 >= ti.rows) break;
-            uint32_t v[CW], lo[CW];
-            tmem_ld16(d + (MODE == kMxDigits ? 8 : 1) * c0, v);
-            if constexpr (PARTS) tmem_ld16(d + mx_pad16(ti.rows) + c0, lo);
-            tmem_wait_ld();
+            if constexpr (MODE == kMxA4) {
+                tmem_ld16(d + c0, sum[j]);  // there after the wait below
+            } else if constexpr (PARTS) {
+                uint32_t v[CW], lo[CW];
+                tmem_ld16(d + c0, v);
+                tmem_ld16(d + n16 + c0, lo);
+                tmem_wait_ld();
+#pragma unroll
+                for (int i = 0; i < TW; ++i) sum[j][i] = __float_as_uint(__uint_as_float(v[i]) + __uint_as_float(lo[i]));
+            } else {
+                uint32_t v[CW];
+                tmem_ld16(d + 8 * c0, v);
+                tmem_wait_ld();
+#pragma unroll
+                for (int i = 0; i < TW; ++i) {  // small digits first
+                    const uint32_t* w = v + 8 * i;
+                    sum[j][i] = __float_as_uint((__uint_as_float(w[0]) + __uint_as_float(w[1])) +
+                                                ((__uint_as_float(w[2]) + __uint_as_float(w[3])) +
+                                                 ((__uint_as_float(w[4]) + __uint_as_float(w[5])) +
+                                                  (__uint_as_float(w[6]) + __uint_as_float(w[7])))));
+                }
+            }
+        }
+        if constexpr (MODE == kMxA4) tmem_wait_ld();
+    }
+
+    // n: this lane's output; add: the sums are of a part of K.
+    __device__ __forceinline__ void store(const MxGemm& g, const Tile& ti, int h, int n, bool add) const {
+#pragma unroll
+        for (int j = 0; j < READS; ++j) {
+            if ((2 * j + h) * TW >= ti.rows) break;
 #pragma unroll
             for (int i = 0; i < TW; ++i) {
                 const int m = j * TW + i;
                 const int row = __shfl_sync(kFull, to[m / 32], m % 32);
-                float f = __uint_as_float(v[i]);
-                if constexpr (PARTS) f += __uint_as_float(lo[i]);
-                if constexpr (MODE == kMxDigits) {  // small digits first
-                    const uint32_t* w = v + 8 * i;
-                    f = ((__uint_as_float(w[0]) + __uint_as_float(w[1])) +
-                         ((__uint_as_float(w[2]) + __uint_as_float(w[3])) +
-                          ((__uint_as_float(w[4]) + __uint_as_float(w[5])) +
-                           (__uint_as_float(w[6]) + __uint_as_float(w[7]))))) *
-                        __shfl_sync(kFull, factor[m / 32], m % 32);
-                }
+                float s = __uint_as_float(sum[j][i]);
+                if constexpr (MODE == kMxDigits) s *= __shfl_sync(kFull, factor[m / 32], m % 32);
                 float* const y = g.y + (long long)row * g.N + n;
                 if (row >= 0 && n < g.N) {
-                    if (add) atomicAdd(y, f);
-                    else *y = f;
+                    if (add) atomicAdd(y, s);
+                    else *y = s;
                 }
             }
         }

@@ -247,7 +247,8 @@ cudaError_t launch_mx_dequant(const uint8_t* codes, const uint8_t* scales, int N
 // How the product takes x (see mx_layout.cuh): 4-bit, or 16-bit as eight 4-bit digits or as two 8-bit parts.
 enum MxMode { kMxA4 = 0, kMxDigits = 1, kMxParts = 2 };
 __host__ __device__ constexpr int mx_planes(int mode) { return mode == kMxA4 ? 1 : mode == kMxDigits ? 8 : 2; }
-constexpr int kMxRows = 192;   // operand rows of a token block at most
+constexpr int kMxRows = 256;   // operand rows of a token block at most,
+constexpr int kMxRows2 = 192;  // and with two accumulators to a CTA
 constexpr int kMxTopk = 64;    // pairs of a token at most
 // What the host decides for a product over R rows: the mode, the tokens of a block at most, scale blocks per 128
 // columns of a slot, and whether tiles may be cut along K between two CTAs (y is then zeroed by the quantiser).
