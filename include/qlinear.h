@@ -177,9 +177,11 @@ int qlinear_workspace_size(int fmt, int flags, int M, int N, int K, size_t* byte
  *      exact in int32 before its two scales are applied; the same for int5
  *      with M >= 65 (W5A8, codes q - z).  QL_MXFP4A4_G32: x~ is
  *      act_quant_mxfp4 of (rotated) x.  QL_MXFP4_G32: x~ enters the tensor
- *      cores as two E4M3 parts under one power-of-two scale per 32 values,
- *      whose sum is exact for every value at least 2^-14 of the largest of its
- *      32 and within 2^-22 of that largest otherwise.
+ *      cores as eight 4-bit digits (few rows) or two 8-bit parts, each with a
+ *      power-of-two scale per 32 values; their sum is exact for every value at
+ *      least 2^-14 of the largest of its 32 and within 2^-22 of that largest
+ *      otherwise.  (Digits of a block below 2^-105 in a row that reaches 2^-64
+ *      end at 2^-129.)
  *   W_packed, scales, zeros: the packed weight (zeros only for int5).
  *   ws, ws_bytes: caller's device workspace, at least qlinear_workspace_size.
  * y is overwritten.  The floating-point sums may be accumulated in any order;
@@ -188,10 +190,14 @@ int qlinear_workspace_size(int fmt, int flags, int M, int N, int K, size_t* byte
  * int5 up to 64 rows) stage one token row, in fp32 and f16, in shared memory:
  * they take K <= QL_A16_MAX_K and return QL_EUNSUPPORTED above it
  * (moe_gate_up likewise).  The MXFP4 formats have no such limit here.
- * MXFP4: W_packed is 32-byte aligned (QL_EALIGN otherwise); a row of x with
+ * MXFP4: W_packed is 32-byte aligned (QL_EALIGN otherwise), and rows of x and
+ * of the weight (of all experts together) number at most QL_MXFP4_MAX_ROWS
+ * (QL_EUNSUPPORTED above, in every MXFP4 call); a row of x with
  * a value that is not finite gives a row of y that is NaN, and a weight block
- * with scale byte 255 a NaN column; the sums are bit-reproducible. */
-enum { QL_A16_MAX_K = 32768 };
+ * with scale byte 255 a NaN column; a sum that leaves fp32's range on the way is
+ * infinite or NaN, and results below 2^-126 may be flushed to zero; the sums are
+ * bit-reproducible. */
+enum { QL_A16_MAX_K = 32768, QL_MXFP4_MAX_ROWS = 1 << 30 };
 int qlinear_forward(const void* x, const void* W_packed, const void* scales, const uint8_t* zeros, int fmt,
                     int flags, int M, int N, int K, float* y, void* ws, size_t ws_bytes, void* stream);
 

@@ -187,6 +187,8 @@ MxWs mx_ws(int fmt, int R, int N, int K, int E, bool pairs) {
     return w;
 }
 
+bool mx_too_many(long long rows) { return rows > QL_MXFP4_MAX_ROWS; }
+
 // Quantise the activations, then the product.  E = 0: one weight over every row.
 int mx_product(const void* x, const void* codes, const void* scales, int flags, int R, int N, int K, int E,
                const int32_t* offsets, const int32_t* perm, const int32_t* ids, int topk, const MxWs& w, uint8_t* ws,
@@ -269,6 +271,7 @@ int check_experts(const ql_experts* ex) {
         ex->fmt != QL_FP8A8_B128_BF16 && !fmt_mxfp4(ex->fmt))
         return QL_EUNSUPPORTED;
     if (ex->K > QL_A16_MAX_K) return QL_EUNSUPPORTED;
+    if (fmt_mxfp4(ex->fmt) && mx_too_many((long long)ex->E * ex->N)) return QL_EUNSUPPORTED;
     if (!ex->codes || !ex->scales) return QL_EINVAL;
     if (!aligned_codes(ex->fmt, ex->codes) || !aligned16(ex->scales)) return QL_EALIGN;
     return QL_OK;
@@ -341,6 +344,7 @@ int qlinear_pack(const float* W, const void* codes_in, const void* scales_in, co
                  int flags, int N, int K, void* codes_out, void* scales_out, uint8_t* zeros_out, void* stream) {
     if (!fmt_valid(fmt) || N < 1 || K < 128 || K % 128 || (flags & ~(QL_HADAMARD | QL_SCALE_SEARCH)))
         return QL_EINVAL;
+    if (fmt_mxfp4(fmt) && mx_too_many(N)) return QL_EUNSUPPORTED;
     if (!codes_out || !scales_out) return QL_EINVAL;
     if ((W == nullptr) == (codes_in == nullptr)) return QL_EINVAL;  // exactly one source
     if (flags & QL_SCALE_SEARCH) {  // a rule for quantising W, int8 formats only
@@ -401,6 +405,7 @@ int qlinear_workspace_size(int fmt, int flags, int M, int N, int K, size_t* byte
     if (!fmt_valid(fmt) || M < 1 || N < 1 || K < 128 || K % 128 || (flags & ~(QL_HADAMARD | QL_SCALE_SEARCH)) ||
         !bytes)
         return QL_EINVAL;
+    if (fmt_mxfp4(fmt) && (mx_too_many(M) || mx_too_many(N))) return QL_EUNSUPPORTED;
     *bytes = fmt_mxfp4(fmt) ? mx_ws(fmt, M, N, K, 0, false).total : forward_ws(fmt, M, N, K).total();
     return QL_OK;
 }
@@ -413,6 +418,7 @@ int qlinear_forward(const void* x, const void* W_packed, const void* scales, con
     if (fmt == QL_I5Z_G128_F16 && !zeros) return QL_EINVAL;
     const bool a8 = fmt == QL_I8A8_G128_BF16 || fmt == QL_FP8A8_B128_BF16 || (fmt == QL_I5Z_G128_F16 && M >= kW5A8MinM);
     if (!a8 && !fmt_mxfp4(fmt) && K > QL_A16_MAX_K) return QL_EUNSUPPORTED;
+    if (fmt_mxfp4(fmt) && (mx_too_many(M) || mx_too_many(N))) return QL_EUNSUPPORTED;
     if (!aligned16(x) || !aligned_codes(fmt, W_packed) || !aligned16(scales) || !aligned16(y) ||
         (zeros && !aligned16(zeros)))
         return QL_EALIGN;
@@ -651,6 +657,7 @@ int act_quant_e4m3_g128(const void* x, int M, int K, int rotate, uint8_t* q, flo
 
 int act_quant_mxfp4(const void* x, int M, int K, int rotate, uint8_t* codes, uint8_t* scales, void* stream) {
     if (M < 1 || K < 128 || K % 128 || !x || !codes || !scales) return QL_EINVAL;
+    if (mx_too_many(M)) return QL_EUNSUPPORTED;
     if (!aligned16(x) || !aligned16(codes) || !aligned16(scales)) return QL_EALIGN;
     cudaStream_t st = static_cast<cudaStream_t>(stream);
     const int t = trace_begin(QL_KIND_ACT_QUANT, st);
@@ -661,6 +668,7 @@ int act_quant_mxfp4(const void* x, int M, int K, int rotate, uint8_t* codes, uin
 
 int mxfp4_dequant(const uint8_t* codes, const uint8_t* scales, int N, int K, void* out, void* stream) {
     if (N < 1 || K < 128 || K % 128 || !codes || !scales || !out) return QL_EINVAL;
+    if (mx_too_many(N)) return QL_EUNSUPPORTED;
     if (!aligned16(codes) || !aligned16(scales) || !aligned16(out)) return QL_EALIGN;
     cudaStream_t st = static_cast<cudaStream_t>(stream);
     const int t = trace_begin(QL_KIND_MX_DEQUANT, st);
@@ -698,7 +706,7 @@ int moe_workspace_size(const ql_experts* experts, int T, int topk, size_t* bytes
     int st = check_experts(experts);
     if (st != QL_OK) return st;
     if (T < 1 || topk < 1 || topk > 64 || !bytes) return QL_EINVAL;
-    if (fmt_mxfp4(experts->fmt) && (long long)T * topk > INT32_MAX) return QL_EINVAL;
+    if (fmt_mxfp4(experts->fmt) && mx_too_many((long long)T * topk)) return QL_EUNSUPPORTED;
     *bytes = fmt_mxfp4(experts->fmt) ? mx_ws(experts->fmt, T * topk, experts->N, experts->K, experts->E, true).total
                                      : moe_ws(experts, T, topk).total;
     return QL_OK;
@@ -712,7 +720,7 @@ int moe_gate_up(const void* x, const int32_t* topk_ids, const float* topk_weight
     if (T < 1 || topk < 1 || topk > 64 || !x || !topk_ids || !y) return QL_EINVAL;
     if (!aligned16(x) || !aligned16(topk_ids) || !aligned16(y)) return QL_EALIGN;
     if (fmt_mxfp4(experts->fmt)) {
-        if ((long long)T * topk > INT32_MAX) return QL_EINVAL;
+        if (mx_too_many((long long)T * topk)) return QL_EUNSUPPORTED;
         const int R = T * topk;
         const MxWs w = mx_ws(experts->fmt, R, experts->N, experts->K, experts->E, true);
         if (!ws || ws_bytes < w.total) return QL_EWORKSPACE;
@@ -841,6 +849,7 @@ int qlinear_grouped_workspace_size(const ql_experts* experts, int R, size_t* byt
     if (st != QL_OK) return st;
     if (!fmt_mxfp4(experts->fmt)) return QL_EUNSUPPORTED;
     if (R < 1 || !bytes) return QL_EINVAL;
+    if (mx_too_many(R)) return QL_EUNSUPPORTED;
     *bytes = mx_ws(experts->fmt, R, experts->N, experts->K, experts->E, false).total;
     return QL_OK;
 }
@@ -851,6 +860,7 @@ int qlinear_grouped(const void* x, const int32_t* offsets, const ql_experts* exp
     if (st != QL_OK) return st;
     if (!fmt_mxfp4(experts->fmt)) return QL_EUNSUPPORTED;
     if (R < 1 || !x || !offsets || !y) return QL_EINVAL;
+    if (mx_too_many(R)) return QL_EUNSUPPORTED;
     if (!aligned16(x) || !aligned16(offsets) || !aligned16(y)) return QL_EALIGN;
     const MxWs w = mx_ws(experts->fmt, R, experts->N, experts->K, experts->E, false);
     if (!ws || ws_bytes < w.total) return QL_EWORKSPACE;

@@ -39,6 +39,7 @@ DEVERR_TIMEOUT = 4
 DEVERR_BOUNDS = 8
 
 A16_MAX_K = 32768  # QL_A16_MAX_K: largest K for the formats whose activations stay 16-bit
+MXFP4_MAX_ROWS = 1 << 30  # QL_MXFP4_MAX_ROWS: most rows of x, or of all experts' weights, of an MXFP4 call
 
 STATUS = {0: "QL_OK", 1: "QL_EINVAL", 2: "QL_EUNSUPPORTED", 3: "QL_EALIGN", 4: "QL_EWORKSPACE", 5: "QL_ECUDA",
           6: "QL_EDEVICE"}

@@ -122,7 +122,8 @@ def test_dequant_every_code_and_scale(Q):
     (1, 64, 128, 0), (1, 1000, 5376, 0), (2, 1, 256, 1), (3, 129, 384, 0), (4, 4096, 1152, 1), (15, 128, 640, 0),
     (16, 2048, 5376, 1), (17, 333, 256, 0), (33, 200, 1024, 0), (64, 300, 384, 1), (65, 127, 512, 0),
     (130, 384, 896, 0), (193, 500, 128, 0), (300, 1000, 640, 1), (511, 257, 384, 0), (1290, 640, 256, 0),
-    (2, 19000, 256, 0), (40, 130, 8192, 0)])
+    (2, 19000, 256, 0), (40, 130, 8192, 0), (24, 200, 256, 1), (25, 200, 256, 0), (63, 300, 384, 0), (64, 300, 384, 0),
+    (192, 130, 256, 0), (256, 300, 512, 0), (257, 300, 384, 0), (5, 9473, 128, 0), (70, 9473, 128, 1), (1, 128, 33280, 0)])
 def test_forward(Q, fmt, M, N, K, had):
     x = x_bits(M, K)
     c, s, W = weight(Q, N, K)
@@ -148,7 +149,8 @@ def test_forward_nonfinite_stays_in_its_row_and_column(Q, fmt, M):
     ref, bound = X.forward(x, X.values(n, b), fmt)
     assert np.isnan(ref[2]).all() and np.isnan(ref[4]).all() and np.isnan(ref[:, 7]).all()
     assert np.isnan(ref).sum() == 2 * N + M - 2
-    close(y.astype(np.float64), ref, bound + 2.0 ** -126)  # sums below 2^-126 may be flushed
+    # fp32 atomic adds flush numbers below 2^-126: two partial sums of an output and their sum
+    close(y.astype(np.float64), ref, bound + 3 * 2.0 ** -126)
     assert not y[3, [0, 1, 299]].any()
 
 
@@ -261,6 +263,101 @@ def test_gate_up(Q, fmt, T, topk, E, N, K, had):
         assert Q.ql_get_device_error() == (6, Q.DEVERR_EXPERT_ID)
 
 
+@pytest.mark.parametrize("T,topk,E", [(16, 8, 3), (43, 3, 130), (2, 64, 100), (128, 1, 1024)])
+def test_gate_up_at_the_limit_of_fused_routing(Q, T, topk, E):
+    # 128 and 129 pairs; ids at random, so that a token may name an expert twice, some of no expert
+    N, K, fmt = 130, 256, 16
+    rng = np.random.default_rng(T)
+    ids = rng.integers(-1, E + 1, (T, topk)).astype(np.int32)
+    x = x_bits(T, K, seed=5)
+    c, s, W = weight(Q, N, K, seed=2)
+    c2, s2, W2 = weight(Q, N, K, seed=3)
+    codes, scales = torch.cat([c, c2] * E)[: E * c.numel()], torch.cat([s, s2] * E)[: E * s.numel()]
+    y = torch.full((T, topk, N), float("nan"), device="cuda")
+    Q.moe_gate_up(dev_bf16(x), dev(ids), codes.contiguous(), scales.contiguous(), E, N, fmt=fmt, flags=0, y=y)
+    assert Q.ql_get_device_error() == (6, Q.DEVERR_EXPERT_ID)
+    got = y.cpu().numpy().astype(np.float64)
+    for parity, w in ((0, W), (1, W2)):
+        t, j = np.nonzero((ids >= 0) & (ids < E) & (ids % 2 == parity))
+        close(got[t, j], *X.forward(x[t], w, fmt))
+    t, j = np.nonzero((ids < 0) | (ids >= E))
+    assert not got[t, j].any()
+
+
+# ---- alignment, small magnitudes, waits ------------------------------------------------------------------
+@pytest.mark.parametrize("fmt", FMTS)
+def test_activations_and_weights_16_bytes_off_a_32_byte_boundary(Q, fmt):
+    M, N, K = 9, 140, 384
+    x = x_bits(M, K, seed=8)
+    room = torch.empty(M * K + 8, dtype=torch.bfloat16, device="cuda")
+    xd = room[8:].view(M, K)
+    assert xd.data_ptr() % 32 == 16
+    xd.copy_(dev_bf16(x))
+    n, b = X.quantise(X.bf16_values(x), True)
+    c_ref, s_ref = X.pack(n, b)
+    cq, sq = Q.act_quant_mxfp4(xd, True)
+    assert np.array_equal(host_u8(cq), c_ref.ravel()) and np.array_equal(host_u8(sq), s_ref.ravel())
+    W = synth.weight_rows(3, "mxoff", K, 0, N)
+    wide = torch.empty(N * K + 4, dtype=torch.float32, device="cuda")
+    wd = wide[4:].view(N, K)
+    wd.copy_(dev(W))
+    c, s, _ = Q.qlinear_pack(fmt, N, K, W=wd)
+    c_ref, s_ref = X.pack(*X.quantise(W))
+    assert np.array_equal(host_u8(c), c_ref.ravel()) and np.array_equal(host_u8(s), s_ref.ravel())
+    close(Q.qlinear_forward(xd, c, s, None, fmt, N), *X.forward(x, X.values(*X.quantise(W)), fmt))
+
+
+@pytest.mark.parametrize("rotate", [0, 1])
+@pytest.mark.parametrize("M", [8, 30])
+def test_rows_of_small_magnitude(Q, M, rotate):
+    # 16-bit activations keep what the bound allows from every block of a row, however small the row
+    N, K = 200, 512
+    rng = np.random.default_rng(4)
+    v = rng.standard_normal((M, K))
+    v[1] = np.ldexp(v[1], -110)
+    v[2] = np.ldexp(v[2], -100)
+    v[2, :32] = 0
+    v[3] = np.ldexp(v[3], -126)
+    v[3, 64:96] = np.ldexp(rng.standard_normal(32), -70)
+    v[4, 128:160] = np.ldexp(v[4, 128:160], -120)
+    v[5] = np.ldexp(v[5], -131)
+    v[6] = 0
+    v[7] = np.ldexp(v[7], 100)
+    x = O.bf16_encode(v.ravel()).reshape(M, K)
+    n = rng.integers(0, 16, (N, K), dtype=np.uint8)
+    for scale in (127, 220):
+        W = X.values(n, np.full((N, K // 32), scale, np.uint8))
+        c, s, _ = Q.qlinear_pack(16, N, K, codes=dev(n), scales=dev(np.full((N, K // 32), scale, np.uint8)))
+        ref, bound = X.forward(x, W, 16, bool(rotate))
+        small = np.abs(ref) < 2.0 ** 126  # larger sums overflow fp32 on the way
+        got = Q.qlinear_forward(dev_bf16(x), c, s, None, 16, N, flags=rotate).cpu().numpy().astype(np.float64)
+        # fp32 atomic adds flush numbers below 2^-126: two partial sums of an output, each off by less than that,
+        # and their sum once more, so 3 * 2^-126 at most
+        off = np.abs(got - ref)[small] - bound[small] - 3 * 2.0 ** -126
+        assert off.max() <= 0
+
+
+def test_waits_that_run_out_are_reported(Q):
+    # one row (a tile cut between two CTAs) and many (pairs of CTAs), both formats: with a bound that no wait
+    # meets the calls return and say so, and the same calls are right again afterwards
+    N, K = 600, 640
+    c, s, W = weight(Q, N, K)
+    for fmt in FMTS:
+        for M in (1, 200):
+            x = x_bits(M, K, seed=9)
+            xd = dev_bf16(x)
+            Q.qlinear_forward(xd, c, s, None, fmt, N)
+            assert Q.ql_get_device_error() == (0, 0)
+            Q.ql_set_wait_limit(1)
+            try:
+                Q.qlinear_forward(xd, c, s, None, fmt, N)
+                st, bits = Q.ql_get_device_error()
+            finally:
+                Q.ql_set_wait_limit(0)
+            assert st == 6 and bits == Q.DEVERR_TIMEOUT
+            close(Q.qlinear_forward(xd, c, s, None, fmt, N), *X.forward(x, W, fmt))
+
+
 # ---- together, streams, graphs -----------------------------------------------------------------------------
 @pytest.mark.parametrize("fmt", FMTS)
 def test_experts_block(Q, fmt):
@@ -286,6 +383,25 @@ def test_experts_block(Q, fmt):
     out = Q.moe_down_combine(h, dev(ids), dev(w), dev(wd.view(np.int16)), E).cpu().numpy()
     want = O.moe_down_combine(h.cpu().numpy(), ids, w, wd, E)
     assert np.linalg.norm(out - want) <= 1e-5 * np.linalg.norm(want)
+
+
+@pytest.mark.parametrize("fmt", FMTS)
+def test_two_streams_at_once(Q, fmt):
+    N, K = 2000, 1024
+    c, s, W = weight(Q, N, K)
+    streams = [torch.cuda.Stream() for _ in range(2)]
+    inputs = [x_bits(M, K, seed=10 + M) for M in (4, 150)]
+    xs = [dev_bf16(x) for x in inputs]
+    torch.cuda.synchronize()
+    got = [[], []]
+    for _ in range(10):
+        for i, st in enumerate(streams):
+            with torch.cuda.stream(st):
+                got[i].append(Q.qlinear_forward(xs[i], c, s, None, fmt, N))
+    torch.cuda.synchronize()
+    for x, ys in zip(inputs, got):
+        close(ys[0], *X.forward(x, W, fmt))
+        assert all(torch.equal(ys[0], y) for y in ys[1:])
 
 
 @pytest.mark.parametrize("fmt", FMTS)

@@ -117,6 +117,7 @@ def test_forward_statuses(Q):
         assert call(fmt=fmt, wsb=16) == 4
         assert call(fmt=fmt, ws=P(A + 8)) == 3
         assert call(fmt=fmt, K=32768 + 128, wsb=16) == 4  # no limit on K
+        assert call(fmt=fmt, M=(1 << 30) + 1) == 2 and call(fmt=fmt, N=(1 << 30) + 1) == 2
     assert call(fmt=15) == 1 and call(fmt=18) == 1
 
 
@@ -137,6 +138,10 @@ def test_pack_quantise_and_dequant_statuses(Q):
     assert d(P(A), P(A), 4, 64, P(A), None) == 1
     assert d(P(A), None, 4, 128, P(A), None) == 1
     assert d(P(A), P(A), 4, 128, P(A + 2), None) == 3
+    many = Q.MXFP4_MAX_ROWS + 1
+    assert many == (1 << 30) + 1
+    assert d(P(A), P(A), many, 128, P(A), None) == 2 and q(P(A), many, 128, 0, P(A), P(A), None) == 2
+    assert p(P(A), None, None, None, 16, 0, many, 128, P(A), P(A), None, None) == 2
     assert L.qlinear_gemm_a8(P(A), P(A), P(A), P(A), 17, 4, 64, 256, P(A), 0, None) == 1  # int8 and E4M3 only
 
 
@@ -155,6 +160,7 @@ def test_grouped_and_gate_up_statuses(Q):
     assert grouped(K=200) == 1
     assert grouped(flags=4) == 1
     assert grouped(x=None) == 1 and grouped(off=None) == 1 and grouped(y=None) == 1 and grouped(codes=0) == 1
+    assert grouped(R=(1 << 30) + 1) == 2 and grouped(E=1024, N=(1 << 20) + 1) == 2
     assert grouped(fmt=1) == 2 and grouped(fmt=7) == 2 and grouped(fmt=4) == 2
     assert grouped(codes=A + 16) == 3 and grouped(scales=A + 8) == 3
     assert grouped(off=P(A + 4)) == 3 and grouped(x=P(A + 2)) == 3 and grouped(y=P(A + 4)) == 3
