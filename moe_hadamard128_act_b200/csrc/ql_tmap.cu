@@ -22,10 +22,20 @@ struct TmapKey {
     }
 };
 
+// One entry to a hash of the key: a call looks at one entry for each map, however many weights are in use.
+constexpr int kEntries = 512;
 std::mutex g_mu;
-TmapKey g_keys[128];
-CUtensorMap g_vals[128];
-int g_n = 0, g_next = 0;
+TmapKey g_keys[kEntries];
+CUtensorMap g_vals[kEntries];
+bool g_used[kEntries] = {};
+
+int entry_of(const TmapKey& k) {
+    uint64_t h = reinterpret_cast<uintptr_t>(k.ptr) >> 4;
+    for (const uint64_t v : {(uint64_t)k.rows, (uint64_t)k.width, (uint64_t)k.ld,
+                             (uint64_t)k.box_x << 32 | (uint64_t)k.box_y << 16 | (uint64_t)k.swz << 8 | (uint64_t)k.type})
+        h = (h ^ v) * 0x9E3779B97F4A7C15ull;
+    return (int)(h >> 55);
+}
 PFN_cuTensorMapEncodeTiled_v12000 g_encode = nullptr;
 
 // width and box_x in elements, ld in bytes.
@@ -33,11 +43,11 @@ cudaError_t make_tmap(const void* base, CUtensorMapDataType type, long long rows
                       int box_x, int box_y, int swz, CUtensorMap* out) {
     std::lock_guard<std::mutex> lock(g_mu);
     const TmapKey key{base, rows, width, ld_bytes, box_x, box_y, swz, type};
-    for (int i = 0; i < g_n; ++i)
-        if (g_keys[i] == key) {
-            *out = g_vals[i];
-            return cudaSuccess;
-        }
+    const int at = entry_of(key);
+    if (g_used[at] && g_keys[at] == key) {
+        *out = g_vals[at];
+        return cudaSuccess;
+    }
     if (!g_encode) {
         cudaDriverEntryPointQueryResult q;
         void* fn = nullptr;
@@ -57,9 +67,9 @@ cudaError_t make_tmap(const void* base, CUtensorMapDataType type, long long rows
                                 CU_TENSOR_MAP_INTERLEAVE_NONE, static_cast<CUtensorMapSwizzle>(swz),
                                 CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
     if (r != CUDA_SUCCESS) return cudaErrorInvalidValue;
-    const int slot = g_n < 128 ? g_n++ : (g_next++ & 127);
-    g_keys[slot] = key;
-    g_vals[slot] = m;
+    g_keys[at] = key;
+    g_vals[at] = m;
+    g_used[at] = true;
     *out = m;
     return cudaSuccess;
 }

@@ -208,7 +208,7 @@ def qlinear_forward(x: torch.Tensor, codes: torch.Tensor, scales: torch.Tensor, 
         raise ValueError("x must be a 2-D bf16 tensor")
     M, K = x.shape
     if y is None:
-        y = torch.empty((M, N), dtype=torch.float32, device=x.device)
+        y = torch.empty(M, N, dtype=torch.float32, device=x.device)  # sizes as arguments: faster than a tuple
     need = qlinear_workspace_size(fmt, flags, M, N, K)
     if ws is None or ws.numel() < need:
         ws = _empty(need, x.device)
@@ -310,7 +310,7 @@ def mxfp4_dequant(codes: torch.Tensor, scales: torch.Tensor, N: int, K: int, out
     if codes.numel() * codes.element_size() != cb or scales.numel() * scales.element_size() != sb:
         raise ValueError(f"mxfp4_dequant: [{N}, {K}] takes {cb} code and {sb} scale bytes")
     if out is None:
-        out = torch.empty((N, K), dtype=torch.bfloat16, device=codes.device)
+        out = torch.empty(N, K, dtype=torch.bfloat16, device=codes.device)
     elif out.dtype != torch.bfloat16 or tuple(out.shape) != (N, K):
         raise ValueError(f"out must be a bf16 tensor of shape ({N}, {K})")
     _check("mxfp4_dequant", _on(codes.device, lib().mxfp4_dequant, _ptr(codes), _ptr(scales), N, K, _ptr(out),
@@ -348,7 +348,7 @@ def moe_gate_up(x: torch.Tensor, topk_ids: torch.Tensor, codes: torch.Tensor, sc
     if ws is None or ws.numel() < need:
         ws = _empty(need, x.device)
     if y is None:
-        y = torch.empty((T, topk, N), dtype=torch.float32, device=x.device)
+        y = torch.empty(T, topk, N, dtype=torch.float32, device=x.device)
     st = _on(x.device, lib().moe_gate_up, _ptr(x), _ptr(topk_ids), _ptr(topk_weights), ctypes.byref(ex), T, topk,
              _ptr(y), _ptr(ws), ws.numel(), stream=stream)
     _check("moe_gate_up", st)
@@ -380,7 +380,7 @@ def qlinear_grouped(x: torch.Tensor, offsets: torch.Tensor, codes: torch.Tensor,
     if ws is None or ws.numel() * ws.element_size() < need:
         ws = _empty(need, x.device)
     if y is None:
-        y = torch.empty((R, N), dtype=torch.float32, device=x.device)
+        y = torch.empty(R, N, dtype=torch.float32, device=x.device)
     elif y.dtype != torch.float32 or tuple(y.shape) != (R, N):
         raise ValueError(f"y must be an fp32 tensor of shape ({R}, {N})")
     ex = _experts_struct(E, N, K, fmt, flags, codes, scales)
