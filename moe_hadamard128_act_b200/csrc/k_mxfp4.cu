@@ -138,50 +138,53 @@ __global__ void __launch_bounds__(kActWarps * 32) k_mx_act(const MxAct a) {
     Raw<__nv_bfloat16> raw;  // the next unit's values: on their way while the places are worked out
     auto load = [&]() { raw.load(xr + min(g0 + (int)((threadIdx.x >> 3) & 3), G - 1) * 128 + 16 * lane, wide); };
     load();
-    for (int j = threadIdx.x >> 5; j < dests; j += kActWarps) {
-        const long long y = a.ids ? (long long)x * a.topk + j : x;
-        int r = x, e = 0, first = 0, end = a.R;
-        if (a.ids && !a.inv) {  // few pairs: the pair's place among all, by counting
-            e = __ldg(a.ids + y);
-            r = 0;
-            int size = 0;
+    // Place j: pair (or row) y, at sorted row r of expert e's segment [first, end); r < 0: none.
+    auto place = [&](int j, long long y, int r, int e, int first, int end) {
+        if (r < first || r >= end) r = -1;
+        const int i = r < 0 ? 0 : (r - first) / nt, c = r < 0 ? 0 : (r - first) - i * nt;
+        const long long slot = first / nt + e + i;
+        const int low = mx_pad16(min(nt, end - first - i * nt)) + c;
+        const long long at = MODE == kMxA4 ? (long long)r * (a.K / 2)
+                                           : MODE == kMxDigits ? 4LL * r * a.K : (long long)r * a.K;
+        places[j] = Place{a.codes + at, a.scales + mx_scale_at(slot, G, 0, nblk, MODE == kMxDigits ? 0 : c),
+                          a.scales + mx_scale_at(slot, G, 0, nblk, low), a.y + y * a.N, r, c};
+    };
+    if (a.ids && a.inv) {  // a thread a pair
+        if ((int)threadIdx.x < dests) {
+            const long long y = (long long)x * a.topk + threadIdx.x;
+            int r = __ldg(a.inv + y), first = 0, end = 0;
+            const int e = __ldg(a.ids + y);
+            if (e >= 0 && e < a.E) mx_segment(a.offsets, e, a.R, first, end);
+            place(threadIdx.x, y, r, e, first, end);
+        }
+    } else if (a.ids) {  // few pairs: a warp a pair, its place among all by counting
+        for (int j = threadIdx.x >> 5; j < dests; j += kActWarps) {
+            const long long y = (long long)x * a.topk + j;
+            const int e = __ldg(a.ids + y);
+            int below = 0, size = 0, rank = 0;
             for (int i = threadIdx.x & 31; i < a.R; i += 32) {
                 const int o = __ldg(a.ids + i);
-                first += o >= 0 && o < e;
+                below += o >= 0 && o < e;
                 size += o == e;
-                r += o == e && i < y;
+                rank += o == e && i < y;
             }
-            first = __reduce_add_sync(kFull, first);
-            end = first + __reduce_add_sync(kFull, size);
-            r = first + __reduce_add_sync(kFull, r);
-            if (e < 0 || e >= a.E) {
-                r = -1;
-                if (blockIdx.y == 0) {
-                    for (int n = threadIdx.x & 31; n < a.N; n += 32) a.y[y * a.N + n] = 0.0f;
-                    if ((threadIdx.x & 31) == 0) atomicOr(a.err, (unsigned)QL_DEVERR_EXPERT_ID);
-                }
+            const int first = __reduce_add_sync(kFull, below), end = first + __reduce_add_sync(kFull, size);
+            rank = __reduce_add_sync(kFull, rank);
+            const bool ok = e >= 0 && e < a.E;
+            if ((threadIdx.x & 31) == 0) place(j, y, ok ? first + rank : -1, e, first, end);
+            if (!ok && blockIdx.y == 0) {
+                for (int n = threadIdx.x & 31; n < a.N; n += 32) a.y[y * a.N + n] = 0.0f;
+                if ((threadIdx.x & 31) == 0) atomicOr(a.err, (unsigned)QL_DEVERR_EXPERT_ID);
             }
-        } else if (a.ids) {
-            r = __ldg(a.inv + y);
-            e = __ldg(a.ids + y);
-            if (e < 0 || e >= a.E || r < 0 || r >= a.R) r = -1;
-        } else if (a.offsets) {
-            e = mx_warp_search(a.E, r, [&](int i) { return __ldg(a.offsets + i); });
-            if (e < 0) r = -1;
         }
-        if (a.offsets && r >= 0) {
-            mx_segment(a.offsets, e, a.R, first, end);
-            if (r < first || r >= end) r = -1;  // a row of no expert
+    } else if (threadIdx.x < 32) {
+        int e = 0, first = 0, end = a.R;
+        if (a.offsets) {
+            e = mx_warp_search(a.E, x, [&](int i) { return __ldg(a.offsets + i); });
+            end = 0;
+            if (e >= 0) mx_segment(a.offsets, e, a.R, first, end);  // a row outside it is no expert's
         }
-        const int i = r < 0 ? 0 : (r - first) / nt, c = r < 0 ? 0 : (r - first) - i * nt;
-        if ((threadIdx.x & 31) == 0) {
-            const long long slot = first / nt + e + i;
-            const int low = mx_pad16(min(nt, end - first - i * nt)) + c;
-            const long long at = MODE == kMxA4 ? (long long)r * (a.K / 2)
-                                               : MODE == kMxDigits ? 4LL * r * a.K : (long long)r * a.K;
-            places[j] = Place{a.codes + at, a.scales + mx_scale_at(slot, G, 0, nblk, MODE == kMxDigits ? 0 : c),
-                              a.scales + mx_scale_at(slot, G, 0, nblk, low), a.y + y * a.N, r, c};
-        }
+        if (threadIdx.x == 0) place(0, x, x, e, first, end);
     }
     __syncthreads();
     if (dests == 1 && places[0].row < 0) return;
