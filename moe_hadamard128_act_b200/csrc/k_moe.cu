@@ -44,7 +44,6 @@ __global__ void __launch_bounds__(kPermThreads) k_moe_permute(const int32_t* ids
     extern __shared__ int hist[];  // [E]
     __shared__ int s_red[kPermThreads / 32];
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
-    asm volatile("griddepcontrol.launch_dependents;\n" ::: "memory");  // the MXFP4 quantiser may stand by for the end
     const int P = T * topk;
     const int e = blockIdx.x;  // this CTA's expert; e == E: the bad ids and the totals
 

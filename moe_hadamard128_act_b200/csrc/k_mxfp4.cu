@@ -264,6 +264,99 @@ __global__ void __launch_bounds__(kActWarps * 32) k_mx_act(const MxAct a) {
     }
 }
 
+// The (token, slot) pairs in (expert, pair) order: offsets[E + 1], perm[P], inv[P], as moe_permute makes them, without
+// its counts, chunks and tiles.  A CTA an expert, and one more for the pairs of no expert, which flags them, zeroes
+// their outputs and fills the tail of perm with -1.  Every CTA reads all ids, each warp a run of them 128 at a time:
+// first it counts its expert's pairs and those of the experts before, then, knowing the other warps' counts, it
+// writes.  Bound by latency: 16384 pairs of 128 experts
+// take 6 us less than moe_permute's histogram.
+constexpr int kRouteWarps = 16;
+__global__ void __launch_bounds__(kRouteWarps * 32) k_mx_route(const int32_t* ids, int P, int E, int32_t* offsets,
+                                                               int32_t* perm, int32_t* inv, float* y, int N,
+                                                               unsigned* err) {
+    asm volatile("griddepcontrol.launch_dependents;\n" ::: "memory");  // the quantiser may stand by
+    __shared__ int mine_of[kRouteWarps], below_of[kRouteWarps];
+    const int e = blockIdx.x, warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    const int run = (P + kRouteWarps * 128 - 1) / (kRouteWarps * 128) * 128;
+    const int p0 = warp * run, p1 = min(P, p0 + run);
+    // This lane's four ids of the 128 from p on (E: none, or of no expert; E + 1: past the end).
+    auto load = [&](int p, int id[4]) {
+        const int q = p + 4 * lane;
+        if (q + 3 < P) {
+            const int4 v = __ldg(reinterpret_cast<const int4*>(ids + q));
+            id[0] = v.x; id[1] = v.y; id[2] = v.z; id[3] = v.w;
+        } else {
+#pragma unroll
+            for (int k = 0; k < 4; ++k) id[k] = q + k < P ? __ldg(ids + q + k) : E + 1;
+        }
+#pragma unroll
+        for (int k = 0; k < 4; ++k)
+            if (q + k < P && (id[k] < 0 || id[k] >= E)) id[k] = E;
+    };
+    int mine = 0, below = 0;
+#pragma unroll 4
+    for (int p = p0; p < p1; p += 128) {
+        int id[4];
+        load(p, id);
+#pragma unroll
+        for (int k = 0; k < 4; ++k) {
+            mine += id[k] == e;
+            below += id[k] < e;
+        }
+    }
+    mine = __reduce_add_sync(kFull, mine);
+    below = __reduce_add_sync(kFull, below);
+    if (lane == 0) {
+        mine_of[warp] = mine;
+        below_of[warp] = below;
+    }
+    __syncthreads();
+    int at = 0;  // the sorted row of this warp's first pair
+#pragma unroll
+    for (int w = 0; w < kRouteWarps; ++w) at += below_of[w] + (w < warp ? mine_of[w] : 0);
+    if (threadIdx.x == 0) offsets[e] = at;  // warp 0: the expert's first row; of E: the number of routed pairs
+    if (mine) {
+        int next = at;
+        for (int p = p0; p < p1; p += 128) {
+            int id[4], n = 0;
+            load(p, id);
+#pragma unroll
+            for (int k = 0; k < 4; ++k) n += id[k] == e;
+            if (!__any_sync(kFull, n)) continue;
+            int incl = n;
+#pragma unroll
+            for (int d = 1; d < 32; d <<= 1) {
+                const int up = __shfl_up_sync(kFull, incl, d);
+                if (lane >= d) incl += up;
+            }
+            int r = next + incl - n;
+            next += __shfl_sync(kFull, incl, 31);
+#pragma unroll
+            for (int k = 0; k < 4; ++k) {
+                if (id[k] != e) continue;
+                const int q = p + 4 * lane + k;
+                if (e < E) {
+                    perm[r] = q;
+                    inv[q] = r++;
+                } else {
+                    inv[q] = -1;
+                    for (int i = 0; i < N; ++i) y[(long long)q * N + i] = 0.0f;
+                }
+            }
+        }
+    }
+    if (e == E) {
+        int bad = 0, first = 0;
+#pragma unroll
+        for (int w = 0; w < kRouteWarps; ++w) {
+            bad += mine_of[w];
+            first += below_of[w];
+        }
+        if (bad && threadIdx.x == 0) atomicOr(err, (unsigned)QL_DEVERR_EXPERT_ID);
+        for (int i = first + threadIdx.x; i < P; i += kRouteWarps * 32) perm[i] = -1;
+    }
+}
+
 // Given code numbers (one byte each) two to a byte; numbers above 15 are packed as 0 and flagged.
 __global__ void __launch_bounds__(256) k_mx_pack_codes(const uint8_t* in, long long n8, uint8_t* out, unsigned* err) {
     const long long i = (long long)blockIdx.x * blockDim.x + threadIdx.x;
@@ -338,6 +431,13 @@ cudaError_t launch_mx_quant_weight(const float* W, int N, int K, int rotate, uin
 cudaError_t launch_mx_quant_rows(const void* x, int M, int K, int rotate, uint8_t* codes, uint8_t* scales,
                                  cudaStream_t s) {
     return quant(static_cast<const __nv_bfloat16*>(x), M, K, rotate, codes, scales, s);
+}
+
+cudaError_t launch_mx_route(const int32_t* ids, int P, int E, int32_t* offsets, int32_t* perm, int32_t* inv, float* y,
+                            int N, unsigned* err, cudaStream_t s) {
+    // Not as a dependent launch: its blocks, waiting beside the product before them, cost that 6 of 87 us.
+    k_mx_route<<<E + 1, kRouteWarps * 32, 0, s>>>(ids, P, E, offsets, perm, inv, y, N, err);
+    return cudaGetLastError();
 }
 
 cudaError_t launch_mx_act(const MxAct& a, cudaStream_t s) {

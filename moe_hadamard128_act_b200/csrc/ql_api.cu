@@ -165,7 +165,7 @@ FwdWs forward_ws(int fmt, size_t M, size_t N, size_t K) {
 // and, for pairs given by routing ids, their permutation.
 struct MxWs {
     MxPlan plan;
-    size_t xq, xs, xf, counts, offsets, perm, inv, total;
+    size_t xq, xs, xf, offsets, perm, inv, total;
 };
 MxWs mx_ws(int fmt, int R, int N, int K, int E, bool pairs) {
     DeviceInfo di;
@@ -176,9 +176,8 @@ MxWs mx_ws(int fmt, int R, int N, int K, int E, bool pairs) {
     w.xq = o; o += align_up((size_t)R * row, 256);
     w.xs = o; o += align_up((size_t)mx_slots(R, E, w.plan.nt) * (K / 128) * w.plan.nblk * 512, 256);
     w.xf = o; o += w.plan.mode == kMxDigits ? align_up((size_t)R * 4, 256) : 0;
-    w.counts = w.offsets = w.perm = w.inv = 0;
+    w.offsets = w.perm = w.inv = 0;
     if (pairs) {
-        w.counts = o; o += align_up((size_t)E * 4, 256);
         w.offsets = o; o += align_up(((size_t)E + 1) * 4, 256);
         w.perm = o; o += align_up((size_t)R * 4, 256);
         w.inv = o; o += align_up((size_t)R * 4, 256);
@@ -730,18 +729,14 @@ int moe_gate_up(const void* x, const int32_t* topk_ids, const float* topk_weight
         if (e != cudaSuccess) return from_cuda(e);
         cudaStream_t s = static_cast<cudaStream_t>(stream);
         uint8_t* const b = static_cast<uint8_t*>(ws);
-        int32_t* const counts = reinterpret_cast<int32_t*>(b + w.counts);
-        int32_t* const offsets = reinterpret_cast<int32_t*>(b + w.offsets);
-        int32_t* const perm = reinterpret_cast<int32_t*>(b + w.perm);
         if (R <= kMxFusedPairs)  // few pairs: the kernels work the places out themselves
             return mx_product(x, experts->codes, experts->scales, experts->flags, R, experts->N, experts->K,
                               experts->E, nullptr, nullptr, topk_ids, topk, w, b, y, di.err_word, s);
-        MoePermuteOut po;
-        po.inv = reinterpret_cast<int32_t*>(b + w.inv);
-        po.yz = y;  // rows of pairs with a bad expert id are zeroed
-        po.N = experts->N;
+        int32_t* const offsets = reinterpret_cast<int32_t*>(b + w.offsets);
+        int32_t* const perm = reinterpret_cast<int32_t*>(b + w.perm);
         const int t = trace_begin(QL_KIND_MOE_PERMUTE, s);
-        e = launch_moe_permute(topk_ids, T, topk, experts->E, counts, offsets, perm, po, di.err_word, s);
+        e = launch_mx_route(topk_ids, R, experts->E, offsets, perm, reinterpret_cast<int32_t*>(b + w.inv), y,
+                            experts->N, di.err_word, s);
         trace_end(t, s);
         if (e != cudaSuccess) return from_cuda(e);
         return mx_product(x, experts->codes, experts->scales, experts->flags, R, experts->N, experts->K,

@@ -263,7 +263,7 @@ def test_gate_up(Q, fmt, T, topk, E, N, K, had):
         assert Q.ql_get_device_error() == (6, Q.DEVERR_EXPERT_ID)
 
 
-@pytest.mark.parametrize("T,topk,E", [(16, 8, 3), (43, 3, 130), (2, 64, 100), (128, 1, 1024)])
+@pytest.mark.parametrize("T,topk,E", [(16, 8, 3), (43, 3, 130), (2, 64, 100), (128, 1, 1024), (700, 4, 37), (513, 1, 9)])
 def test_gate_up_at_the_limit_of_fused_routing(Q, T, topk, E):
     # 128 and 129 pairs; ids at random, so that a token may name an expert twice, some of no expert
     N, K, fmt = 130, 256, 16
