@@ -320,7 +320,9 @@ cudaError_t run(const MxGemm& g, cudaStream_t s) {
     e = PARTS ? make_tmap_u4_spread(g.codes, wrows, g.K, TM, &p.tmW)
               : make_tmap_2d(g.codes, wrows, g.K / 2, g.K / 2, 128, TM, CU_TENSOR_MAP_SWIZZLE_128B, &p.tmW);
     if (e == cudaSuccess) e = make_tmap_2d(g.xq, xrows, xbytes, xbytes, 128, SMALL, CU_TENSOR_MAP_SWIZZLE_128B, &p.tmX);
-    if (e == cudaSuccess) e = make_tmap_2d(g.xq, xrows, xbytes, xbytes, 128, BIG, CU_TENSOR_MAP_SWIZZLE_128B, &p.tmXb);
+    p.tmXb = p.tmX;
+    if (e == cudaSuccess && rows >= BIG)
+        e = make_tmap_2d(g.xq, xrows, xbytes, xbytes, 128, BIG, CU_TENSOR_MAP_SWIZZLE_128B, &p.tmXb);
     if (e != cudaSuccess) return e;
 
     static bool attr_set[64] = {};

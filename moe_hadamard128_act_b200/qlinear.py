@@ -133,19 +133,26 @@ def _ptr(t: torch.Tensor | None):
     return t.data_ptr()
 
 
+_device = torch._C._cuda_getDevice
+_raw_stream = torch._C._cuda_getCurrentRawStream
+
+
 def _stream(stream=None):
     """Address of the stream, or of the current device's current one."""
-    if stream is not None:
-        return stream.cuda_stream
-    return torch._C._cuda_getCurrentRawStream(torch._C._cuda_getDevice())
+    return _raw_stream(_device()) if stream is None else stream.cuda_stream
 
 
-def _on(device, fn, *args, stream=None) -> int:
-    """fn(*args, stream) on the tensors' device, whichever device is the current one."""
-    if device.index == torch._C._cuda_getDevice():
-        return fn(*args, _stream(stream))
-    with torch.cuda.device(device):
-        return fn(*args, _stream(stream))
+def _on(device, name: str, *args, stream=None):
+    """Call the library's function on the tensors' device, whichever device is the current one."""
+    fn = getattr(_lib or lib(), name)
+    index = device.index
+    if index == _device():
+        st = fn(*args, _raw_stream(index) if stream is None else stream.cuda_stream)
+    else:
+        with torch.cuda.device(device):
+            st = fn(*args, _stream(stream))
+    if st != 0:
+        raise QLError(name, st)
 
 
 def _empty(nbytes: int, device) -> torch.Tensor:
@@ -212,9 +219,8 @@ def qlinear_forward(x: torch.Tensor, codes: torch.Tensor, scales: torch.Tensor, 
     need = qlinear_workspace_size(fmt, flags, M, N, K)
     if ws is None or ws.numel() < need:
         ws = _empty(need, x.device)
-    st = _on(x.device, lib().qlinear_forward, _ptr(x), _ptr(codes), _ptr(scales), _ptr(zeros), fmt, flags, M, N, K,
-             _ptr(y), _ptr(ws), ws.numel(), stream=stream)
-    _check("qlinear_forward", st)
+    _on(x.device, "qlinear_forward", _ptr(x), _ptr(codes), _ptr(scales), _ptr(zeros), fmt, flags, M, N, K, _ptr(y),
+        _ptr(ws), ws.numel(), stream=stream)
     return y
 
 
@@ -298,8 +304,7 @@ def act_quant_mxfp4(x: torch.Tensor, rotate: bool = False, stream=None):
     M, K = _rows(x, "act_quant_mxfp4")
     cb, sb, _ = qlinear_packed_sizes(MXFP4_G32, M, K)
     codes, scales = _empty(cb, x.device), _empty(sb, x.device)
-    _check("act_quant_mxfp4", _on(x.device, lib().act_quant_mxfp4, _ptr(x), M, K, int(rotate), _ptr(codes),
-                                  _ptr(scales), stream=stream))
+    _on(x.device, "act_quant_mxfp4", _ptr(x), M, K, int(rotate), _ptr(codes), _ptr(scales), stream=stream)
     return codes, scales
 
 
@@ -313,8 +318,7 @@ def mxfp4_dequant(codes: torch.Tensor, scales: torch.Tensor, N: int, K: int, out
         out = torch.empty(N, K, dtype=torch.bfloat16, device=codes.device)
     elif out.dtype != torch.bfloat16 or tuple(out.shape) != (N, K):
         raise ValueError(f"out must be a bf16 tensor of shape ({N}, {K})")
-    _check("mxfp4_dequant", _on(codes.device, lib().mxfp4_dequant, _ptr(codes), _ptr(scales), N, K, _ptr(out),
-                                stream=stream))
+    _on(codes.device, "mxfp4_dequant", _ptr(codes), _ptr(scales), N, K, _ptr(out), stream=stream)
     return out
 
 
@@ -349,9 +353,8 @@ def moe_gate_up(x: torch.Tensor, topk_ids: torch.Tensor, codes: torch.Tensor, sc
         ws = _empty(need, x.device)
     if y is None:
         y = torch.empty(T, topk, N, dtype=torch.float32, device=x.device)
-    st = _on(x.device, lib().moe_gate_up, _ptr(x), _ptr(topk_ids), _ptr(topk_weights), ctypes.byref(ex), T, topk,
-             _ptr(y), _ptr(ws), ws.numel(), stream=stream)
-    _check("moe_gate_up", st)
+    _on(x.device, "moe_gate_up", _ptr(x), _ptr(topk_ids), _ptr(topk_weights), ctypes.byref(ex), T, topk, _ptr(y),
+        _ptr(ws), ws.numel(), stream=stream)
     return y
 
 
@@ -384,8 +387,8 @@ def qlinear_grouped(x: torch.Tensor, offsets: torch.Tensor, codes: torch.Tensor,
     elif y.dtype != torch.float32 or tuple(y.shape) != (R, N):
         raise ValueError(f"y must be an fp32 tensor of shape ({R}, {N})")
     ex = _experts_struct(E, N, K, fmt, flags, codes, scales)
-    _check("qlinear_grouped", _on(x.device, lib().qlinear_grouped, _ptr(x), _ptr(offsets), ctypes.byref(ex), R,
-                                  _ptr(y), _ptr(ws), ws.numel() * ws.element_size(), stream=stream))
+    _on(x.device, "qlinear_grouped", _ptr(x), _ptr(offsets), ctypes.byref(ex), R, _ptr(y), _ptr(ws),
+        ws.numel() * ws.element_size(), stream=stream)
     return y
 
 
