@@ -351,32 +351,64 @@ cudaError_t run(const MxGemm& g, cudaStream_t s) {
 
 }  // namespace
 
-// Tokens of a block: the widest the accumulators allow, cut evenly over one weight's rows; for experts twice the
-// average count, so that most experts are one block (a block costs its own rows alone, but a second one reads
-// the weights again), or 1.6 times with digits, whose rows take ring slots from the weights (128 experts of 1408 x
-// 2816, 200 tokens: 63.2 us against 65.2).
-MxPlan mx_plan(bool a16, int R, int N, int K, int E, int sms) {
-    (void)K;
+namespace {
+
+constexpr int kPlanSms = 148;  // a plan goes by this GPU's count, so that a workspace size does not depend on a device
+
+// Tokens of a block for `experts` weights of R rows each on pairs of CTAs: the cut with the least rounds of tiles
+// times what a tile of so many operand rows takes.  Measured at 5376 columns, 74 x 256 weight rows and 2048 rows of
+// 4-bit x, a round of 64, 96, 128, 160, 192, 208 and 256 operand rows takes 5.4, 6.1, 6.1, 7.0, 8.4, 8.8 and 9.9 us,
+// one of 16-bit parts the same in proportion.
+int pair_tokens(int P, long long R, int N, int experts) {
+    const long long wide = kMxRows / P, first = (R + wide - 1) / wide, blocks_n = (N + 2 * TM - 1) / (2 * TM);
+    long long best = 0, nt = 0;
+    for (long long b = first; b <= 4 * first + 8; ++b) {
+        const long long t = ((R + b - 1) / b + 15) / 16 * 16, rows = P * t;
+        if (nt && rows < 64) break;
+        const long long tiles = blocks_n * experts * ((R + t - 1) / t), rounds = (tiles + kPlanSms / 2 - 1) / (kPlanSms / 2);
+        const long long cost = rounds * (rows <= 128 ? 200 + rows * 2 / 5 : 150 + rows);
+        if (!nt || cost < best) {
+            best = cost;
+            nt = t;
+        }
+    }
+    return (int)nt;
+}
+
+}  // namespace
+
+MxPlan mx_plan(bool a16, int R, int N, int E) {
     MxPlan p;
-    const long long per = E ? (R + E - 1) / E : R;  // rows an expert
+    const long long per = E ? ((long long)R + E - 1) / E : R;  // rows an expert
     // Digits up to two blocks of one weight (21504 x 5376 at 32 rows 24.9 us against 26.5, at 48 rows 27.1 against
     // 28.6, at 64 rows parts take 27.3), or 20 rows an expert (128 of 1408 x 2816 at 280 tokens 70.6 against 76.7, at
     // 384 tokens 88.0 against 79.9).
     p.mode = !a16 ? kMxA4 : per <= (E ? 20 : 48) ? kMxDigits : kMxParts;
-    const int P = mx_planes(p.mode), most = (p.mode == kMxDigits || E ? kMxRows2 : kMxRows) / P, step = p.mode == kMxDigits ? 2 : 16;
-    long long nt = E ? (p.mode == kMxDigits ? (8 * per + 4) / 5 : 2 * per) : (R + (R + most - 1LL) / most - 1) / ((R + most - 1LL) / most);
-    if (nt > most) nt = most;
-    p.nt = (int)((nt + step - 1) / step * step);
+    const int P = mx_planes(p.mode);
+    if (p.mode == kMxDigits) {
+        // Cut evenly, an even number of tokens; for experts 1.6 times the average count, so that most are one block (a
+        // block costs its own rows alone, but a second one reads the weights again) and few ring slots go to rows
+        // that are not there (128 experts of 1408 x 2816, 200 tokens: 63.2 us against 65.2 at twice the average).
+        const long long most = kMxRows2 / P, b = (R + most - 1) / most, nt = E ? (8 * per + 4) / 5 : (R + b - 1) / b;
+        p.nt = (int)(((nt < most ? nt : most) + 1) / 2 * 2);
+        p.pair = 0;
+    } else if (E && per * P < kMxRows2) {
+        const long long most = kMxRows2 / P;
+        p.nt = (int)((2 * per < most ? 2 * per : most) + 15) / 16 * 16;
+        // Experts with 4-bit activations wait for their weights longer than for their rows: pairs of CTAs take 128 of
+        // 1408 x 2816 at 400 tokens to 60.8 us from 58.9, at 2048 tokens to 91.5 from 94; parts gain everywhere (400
+        // tokens 80 against 96).
+        p.pair = P * p.nt >= (p.mode == kMxA4 ? kMxRows2 : 64);
+    } else {
+        // Pairs once a token block is wide enough for its operand stream to count: 21504 x 5376 at 64 rows 20.5 us
+        // against 22.3, at 192 rows 27.1 against 30.6.
+        p.nt = pair_tokens(P, per, N, E ? E : 1);
+        p.pair = P * p.nt >= 64;
+    }
     p.nblk = (P * p.nt + 127) / 128;
     // Cutting tiles along K costs a zeroed y: worth it while y is small beside the weights.
     const long long tiles = (long long)((N + TM - 1) / TM) * mx_slots(R, 0, p.nt);
-    p.split = (long long)R * N * 4 <= (4 << 20) && (E || tiles < 8LL * sms);
-    // Two CTAs to a tile once a token block is wide enough for its operand stream to count: 21504 x 5376 at 64 rows
-    // 20.5 us against 22.3, at 192 rows 27.1 against 30.6.  Experts with 4-bit activations wait for their weights
-    // longer (128 of 1408 x 2816 at 400 tokens 60.8 against 58.9, at 2048 tokens 91.5 against 94); 16-bit parts gain
-    // everywhere (400 tokens 80 against 96).
-    p.pair = p.mode != kMxDigits && p.nt * P >= (E && p.mode == kMxA4 ? kMxRows2 : 64);
-    if (p.pair) p.split = 0;
+    p.split = !p.pair && (long long)R * N * 4 <= (4 << 20) && (E || tiles < 8LL * kPlanSms);
     return p;
 }
 

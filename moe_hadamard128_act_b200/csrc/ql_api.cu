@@ -168,9 +168,8 @@ struct MxWs {
     size_t xq, xs, xf, offsets, perm, inv, total;
 };
 MxWs mx_ws(int fmt, int R, int N, int K, int E, bool pairs) {
-    DeviceInfo di;
     MxWs w;
-    w.plan = mx_plan(fmt == QL_MXFP4_G32, R, N, K, E, device_info(&di) == cudaSuccess ? di.sm_count : 148);
+    w.plan = mx_plan(fmt == QL_MXFP4_G32, R, N, E);
     const size_t row = w.plan.mode == kMxA4 ? K / 2 : w.plan.mode == kMxDigits ? (size_t)4 * K : (size_t)2 * K;
     size_t o = 0;
     w.xq = o; o += align_up((size_t)R * row, 256);

@@ -255,7 +255,7 @@ constexpr int kMxTopk = 64;    // pairs of a token at most
 struct MxPlan {
     int mode, nt, nblk, split, pair;  // pair: two CTAs to a tile (launch_mx_pair)
 };
-MxPlan mx_plan(bool a16, int R, int N, int K, int E, int sms);
+MxPlan mx_plan(bool a16, int R, int N, int E);
 inline long long mx_slots(int R, int E, int nt) { return E ? (long long)R / nt + E + 1 : ((long long)R + nt - 1) / nt; }
 // The product's activations: R sorted rows.  Rows of x are sorted rows themselves (ids null; offsets [E + 1] null:
 // one expert owns all), or tokens whose topk pairs, of experts ids[t * topk + j], sit at sorted rows
