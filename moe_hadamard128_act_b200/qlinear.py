@@ -159,6 +159,27 @@ def _empty(nbytes: int, device) -> torch.Tensor:
     return torch.empty(max(int(nbytes), 16), dtype=torch.uint8, device=device)
 
 
+def _new(stream, device, dtype, *size) -> torch.Tensor:
+    """A tensor of the stream that the call runs on, so that its memory is not handed on while the call runs."""
+    if stream is None:
+        return torch.empty(*size, dtype=dtype, device=device)  # sizes as arguments: faster than a tuple
+    with torch.cuda.stream(stream):
+        return torch.empty(*size, dtype=dtype, device=device)
+
+
+def _is_mxfp4(fmt: int) -> bool:
+    return fmt == MXFP4_G32 or fmt == MXFP4A4_G32
+
+
+def _mx_check(what: str, fmt: int, N: int, K: int, E: int, codes, scales, y, shape):
+    """The product's tensors have the sizes that its kernels take for granted."""
+    cb, sb, _ = qlinear_packed_sizes(fmt, N, K)
+    if codes.nbytes != E * cb or scales.nbytes != E * sb:
+        raise ValueError(f"{what}: {E} x [{N}, {K}] take {E * cb} code and {E * sb} scale bytes")
+    if y is not None and (y.dtype != torch.float32 or y.shape != shape):
+        raise ValueError(f"{what}: y must be an fp32 tensor of shape {tuple(shape)}")
+
+
 # ---- sizes: functions of their arguments alone, remembered so that a call does not ask again ----------
 @lru_cache(maxsize=4096)
 def qlinear_packed_sizes(fmt: int, N: int, K: int):
@@ -198,11 +219,15 @@ def qlinear_pack(fmt: int, N: int, K: int, W: torch.Tensor | None = None, codes:
     uint8 tensors of the packed byte sizes (zeros is None except for int5)."""
     dev = (W if W is not None else codes).device
     cb, sb, zb = qlinear_packed_sizes(fmt, N, K)
-    c_out, s_out = _empty(cb, dev), _empty(sb, dev)
-    z_out = _empty(zb, dev) if zb else None
-    st = lib().qlinear_pack(_ptr(W), _ptr(codes), _ptr(scales), _ptr(zeros), fmt, flags, N, K, _ptr(c_out),
-                            _ptr(s_out), _ptr(z_out), _stream(stream))
-    _check("qlinear_pack", st)
+    if _is_mxfp4(fmt):
+        if W is not None and (W.dtype != torch.float32 or W.numel() != N * K):
+            raise ValueError(f"W must be an fp32 tensor of shape ({N}, {K})")
+        if codes is not None and (codes.nbytes != N * K or scales is None or scales.nbytes != N * K // 32):
+            raise ValueError(f"[{N}, {K}] take {N * K} code numbers and {N * K // 32} scales, a byte each")
+    c_out, s_out = (_new(stream, dev, torch.uint8, max(n, 16)) for n in (cb, sb))
+    z_out = _new(stream, dev, torch.uint8, max(zb, 16)) if zb else None
+    _on(dev, "qlinear_pack", _ptr(W), _ptr(codes), _ptr(scales), _ptr(zeros), fmt, flags, N, K, _ptr(c_out),
+        _ptr(s_out), _ptr(z_out), stream=stream)
     return c_out[:cb], s_out[:sb], (z_out[:zb] if z_out is not None else None)
 
 
@@ -214,11 +239,13 @@ def qlinear_forward(x: torch.Tensor, codes: torch.Tensor, scales: torch.Tensor, 
     if x.dtype != torch.bfloat16 or x.dim() != 2:
         raise ValueError("x must be a 2-D bf16 tensor")
     M, K = x.shape
+    if _is_mxfp4(fmt):
+        _mx_check("qlinear_forward", fmt, N, K, 1, codes, scales, y, (M, N))
     if y is None:
-        y = torch.empty(M, N, dtype=torch.float32, device=x.device)  # sizes as arguments: faster than a tuple
+        y = _new(stream, x.device, torch.float32, M, N)
     need = qlinear_workspace_size(fmt, flags, M, N, K)
     if ws is None or ws.numel() < need:
-        ws = _empty(need, x.device)
+        ws = _new(stream, x.device, torch.uint8, max(need, 16))
     _on(x.device, "qlinear_forward", _ptr(x), _ptr(codes), _ptr(scales), _ptr(zeros), fmt, flags, M, N, K, _ptr(y),
         _ptr(ws), ws.numel(), stream=stream)
     return y
@@ -303,7 +330,7 @@ def act_quant_mxfp4(x: torch.Tensor, rotate: bool = False, stream=None):
     """MXFP4 codes and scales (uint8, packed layouts for M rows) of bf16 x [M, K]."""
     M, K = _rows(x, "act_quant_mxfp4")
     cb, sb, _ = qlinear_packed_sizes(MXFP4_G32, M, K)
-    codes, scales = _empty(cb, x.device), _empty(sb, x.device)
+    codes, scales = (_new(stream, x.device, torch.uint8, n) for n in (cb, sb))
     _on(x.device, "act_quant_mxfp4", _ptr(x), M, K, int(rotate), _ptr(codes), _ptr(scales), stream=stream)
     return codes, scales
 
@@ -312,10 +339,10 @@ def mxfp4_dequant(codes: torch.Tensor, scales: torch.Tensor, N: int, K: int, out
                   stream=None) -> torch.Tensor:
     """The bf16 values [N, K] that packed MXFP4 codes and scales stand for."""
     cb, sb, _ = qlinear_packed_sizes(MXFP4_G32, N, K)
-    if codes.numel() * codes.element_size() != cb or scales.numel() * scales.element_size() != sb:
+    if codes.nbytes != cb or scales.nbytes != sb:
         raise ValueError(f"mxfp4_dequant: [{N}, {K}] takes {cb} code and {sb} scale bytes")
     if out is None:
-        out = torch.empty(N, K, dtype=torch.bfloat16, device=codes.device)
+        out = _new(stream, codes.device, torch.bfloat16, N, K)
     elif out.dtype != torch.bfloat16 or tuple(out.shape) != (N, K):
         raise ValueError(f"out must be a bf16 tensor of shape ({N}, {K})")
     _on(codes.device, "mxfp4_dequant", _ptr(codes), _ptr(scales), N, K, _ptr(out), stream=stream)
@@ -347,12 +374,17 @@ def moe_gate_up(x: torch.Tensor, topk_ids: torch.Tensor, codes: torch.Tensor, sc
     """y [T, topk, N] fp32 for stacked expert weights (codes [E*N*K], scales)."""
     T, K = x.shape
     topk = topk_ids.shape[1]
+    if _is_mxfp4(fmt):
+        _rows(x, "moe_gate_up")
+        if topk_ids.dtype != torch.int32 or topk_ids.shape != (T, topk):
+            raise ValueError(f"topk_ids must be an int32 tensor of shape ({T}, topk)")
+        _mx_check("moe_gate_up", fmt, N, K, E, codes, scales, y, (T, topk, N))
     ex = _experts_struct(E, N, K, fmt, flags, codes, scales)
     need = moe_workspace_size(E, N, K, fmt, flags, T, topk)
     if ws is None or ws.numel() < need:
-        ws = _empty(need, x.device)
+        ws = _new(stream, x.device, torch.uint8, max(need, 16))
     if y is None:
-        y = torch.empty(T, topk, N, dtype=torch.float32, device=x.device)
+        y = _new(stream, x.device, torch.float32, T, topk, N)
     _on(x.device, "moe_gate_up", _ptr(x), _ptr(topk_ids), _ptr(topk_weights), ctypes.byref(ex), T, topk, _ptr(y),
         _ptr(ws), ws.numel(), stream=stream)
     return y
@@ -376,19 +408,15 @@ def qlinear_grouped(x: torch.Tensor, offsets: torch.Tensor, codes: torch.Tensor,
     R, K = _rows(x, "qlinear_grouped")
     if offsets.dtype != torch.int32 or offsets.numel() != E + 1:
         raise ValueError(f"offsets must be an int32 tensor of {E + 1} elements")
-    cb, sb, _ = qlinear_packed_sizes(fmt, N, K)
-    if codes.numel() * codes.element_size() != E * cb or scales.numel() * scales.element_size() != E * sb:
-        raise ValueError(f"{E} experts of [{N}, {K}] take {E * cb} code and {E * sb} scale bytes")
+    _mx_check("qlinear_grouped", fmt, N, K, E, codes, scales, y, (R, N))
     need = qlinear_grouped_workspace_size(E, N, K, fmt, flags, R)
-    if ws is None or ws.numel() * ws.element_size() < need:
-        ws = _empty(need, x.device)
+    if ws is None or ws.nbytes < need:
+        ws = _new(stream, x.device, torch.uint8, max(need, 16))
     if y is None:
-        y = torch.empty(R, N, dtype=torch.float32, device=x.device)
-    elif y.dtype != torch.float32 or tuple(y.shape) != (R, N):
-        raise ValueError(f"y must be an fp32 tensor of shape ({R}, {N})")
+        y = _new(stream, x.device, torch.float32, R, N)
     ex = _experts_struct(E, N, K, fmt, flags, codes, scales)
-    _on(x.device, "qlinear_grouped", _ptr(x), _ptr(offsets), ctypes.byref(ex), R, _ptr(y), _ptr(ws),
-        ws.numel() * ws.element_size(), stream=stream)
+    _on(x.device, "qlinear_grouped", _ptr(x), _ptr(offsets), ctypes.byref(ex), R, _ptr(y), _ptr(ws), ws.nbytes,
+        stream=stream)
     return y
 
 

@@ -186,3 +186,25 @@ def test_binding_refuses_wrong_tensors(Q):
                  lambda: Q.qlinear_grouped(x.to(torch.bfloat16), torch.zeros(3, dtype=torch.int32), u8, u8, 2, 64)):
         with pytest.raises(ValueError):
             call()
+
+
+def test_binding_refuses_tensors_of_other_sizes(Q):
+    import torch
+    x = torch.zeros(4, 128, dtype=torch.bfloat16)
+    c, sc = torch.zeros(64 * 64, dtype=torch.uint8), torch.zeros(512, dtype=torch.uint8)
+    ids = torch.zeros(4, 2, dtype=torch.int32)
+    y = torch.zeros(4, 63)
+    for fmt in (Q.MXFP4_G32, Q.MXFP4A4_G32):
+        for call in (lambda: Q.qlinear_forward(x, c[:-1], sc, None, fmt, 64),
+                     lambda: Q.qlinear_forward(x, c, sc[:-1], None, fmt, 64),
+                     lambda: Q.qlinear_forward(x, c, sc, None, fmt, 64, y=y),
+                     lambda: Q.moe_gate_up(x, ids, c, sc, 2, 64, fmt=fmt),
+                     lambda: Q.moe_gate_up(x, ids.long(), c, sc, 1, 64, fmt=fmt),
+                     lambda: Q.moe_gate_up(x, ids[:3], c, sc, 1, 64, fmt=fmt),
+                     lambda: Q.moe_gate_up(x.float(), ids, c, sc, 1, 64, fmt=fmt),
+                     lambda: Q.moe_gate_up(x, ids, c, sc, 1, 64, fmt=fmt, y=y),
+                     lambda: Q.qlinear_pack(fmt, 64, 128, W=torch.zeros(64, 128, dtype=torch.float16)),
+                     lambda: Q.qlinear_pack(fmt, 64, 128, codes=torch.zeros(64 * 128 - 1, dtype=torch.uint8), scales=sc),
+                     lambda: Q.qlinear_pack(fmt, 64, 128, codes=torch.zeros(64 * 128, dtype=torch.uint8), scales=sc)):
+            with pytest.raises(ValueError, match="take|must be"):
+                call()
