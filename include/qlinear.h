@@ -189,7 +189,7 @@ int qlinear_workspace_size(int fmt, int flags, int M, int N, int K, size_t* byte
  * Calls whose activations stay 16-bit (all formats but W8A8 and format 7, and
  * int5 up to 64 rows) stage one token row, in fp32 and f16, in shared memory:
  * they take K <= QL_A16_MAX_K and return QL_EUNSUPPORTED above it
- * (moe_gate_up likewise).  The MXFP4 formats have no such limit here.
+ * (moe_gate_up likewise).  The MXFP4 formats have no such limit.
  * MXFP4: W_packed is 32-byte aligned (QL_EALIGN otherwise), and rows of x and
  * of the weight (of all experts together) number at most QL_MXFP4_MAX_ROWS
  * (QL_EUNSUPPORTED above, in every MXFP4 call); a row of x with
@@ -309,7 +309,8 @@ int qlinear_grouped_workspace_size(const ql_experts* experts, int R, size_t* byt
  * moe_permute makes them; y fp32 [R, N].  Rows outside every segment (before
  * offsets[0], from offsets[E] on) are neither read nor written.  An expert whose
  * two offsets are out of order or out of [0, R] is skipped and sets
- * QL_DEVERR_BOUNDS.  E <= 1024; `experts` is a host pointer; codes 32-byte aligned. */
+ * QL_DEVERR_BOUNDS; what rows hold that other experts' segments then share is
+ * undefined.  E <= 1024; `experts` is a host pointer; codes 32-byte aligned. */
 int qlinear_grouped(const void* x, const int32_t* offsets, const ql_experts* experts, int R, float* y, void* ws,
                     size_t ws_bytes, void* stream);
 

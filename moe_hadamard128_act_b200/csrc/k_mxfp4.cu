@@ -96,7 +96,7 @@ __global__ void __launch_bounds__(kWarps * 32) k_mx_quant(const T* W, int N, int
 // of x, quantised once and written to every place that the row has among the sorted rows: its own (offsets
 // null, or sorted rows given), or one for each of the token's topk pairs, at the pair's position inv[] in its
 // expert's segment.  Up to kMxFusedPairs pairs come without a permutation: every CTA counts its pairs' places
-// from the ids, and pairs with an id outside [0, E) are flagged and their outputs zeroed here.
+// from the ids and flags those with an id outside [0, E).  The outputs of pairs of no expert are zeroed here.
 struct Place {
     uint8_t *codes, *scale, *low;  // where the row's codes, its scales and its low part's scales begin
     float* y;                      // its output
@@ -172,10 +172,7 @@ __global__ void __launch_bounds__(kActWarps * 32) k_mx_act(const MxAct a) {
             rank = __reduce_add_sync(kFull, rank);
             const bool ok = e >= 0 && e < a.E;
             if ((threadIdx.x & 31) == 0) place(j, y, ok ? first + rank : -1, e, first, end);
-            if (!ok && blockIdx.y == 0) {
-                for (int n = threadIdx.x & 31; n < a.N; n += 32) a.y[y * a.N + n] = 0.0f;
-                if ((threadIdx.x & 31) == 0) atomicOr(a.err, (unsigned)QL_DEVERR_EXPERT_ID);
-            }
+            if (!ok && (threadIdx.x & 31) == 0) atomicOr(a.err, (unsigned)QL_DEVERR_EXPERT_ID);
         }
     } else if (threadIdx.x < 32) {
         int e = 0, first = 0, end = a.R;
@@ -187,14 +184,13 @@ __global__ void __launch_bounds__(kActWarps * 32) k_mx_act(const MxAct a) {
         if (threadIdx.x == 0) place(0, x, x, e, first, end);
     }
     __syncthreads();
-    if (dests == 1 && places[0].row < 0) return;
-    if (a.plan.split) {  // the product adds into these rows
-        for (int j = 0; j < dests; ++j) {
-            if (places[j].row < 0) continue;
-            float* const y = places[j].y;
-            for (int n = blockIdx.y * blockDim.x + threadIdx.x; n < a.N; n += gridDim.y * blockDim.x) y[n] = 0.0f;
-        }
+    for (int j = 0; j < dests; ++j) {
+        // Zeroed: rows that the product adds into, and those of pairs that no expert takes.
+        if (places[j].row < 0 ? !a.ids : !a.plan.split) continue;
+        float* const y = places[j].y;
+        for (int n = blockIdx.y * blockDim.x + threadIdx.x; n < a.N; n += gridDim.y * blockDim.x) y[n] = 0.0f;
     }
+    if (dests == 1 && places[0].row < 0) return;
     while (g0 < G) {
         const int g = g0 + ((threadIdx.x >> 3) & 3);
         const bool first_unit = g0 == 0;
@@ -265,15 +261,14 @@ __global__ void __launch_bounds__(kActWarps * 32) k_mx_act(const MxAct a) {
 }
 
 // The (token, slot) pairs in (expert, pair) order: offsets[E + 1], perm[P], inv[P], as moe_permute makes them, without
-// its counts, chunks and tiles.  A CTA an expert, and one more for the pairs of no expert, which flags them, zeroes
-// their outputs and fills the tail of perm with -1.  Every CTA reads all ids, each warp a run of them 128 at a time:
+// its counts, chunks and tiles.  A CTA an expert, and one more for the pairs of no expert, which flags them and
+// fills the tail of perm with -1.  Every CTA reads all ids, each warp a run of them 128 at a time:
 // first it counts its expert's pairs and those of the experts before, then, knowing the other warps' counts, it
 // writes.  Bound by latency: 16384 pairs of 128 experts
 // take 6 us less than moe_permute's histogram.
 constexpr int kRouteWarps = 16;
 __global__ void __launch_bounds__(kRouteWarps * 32) k_mx_route(const int32_t* ids, int P, int E, int32_t* offsets,
-                                                               int32_t* perm, int32_t* inv, float* y, int N,
-                                                               unsigned* err) {
+                                                               int32_t* perm, int32_t* inv, unsigned* err) {
     asm volatile("griddepcontrol.launch_dependents;\n" ::: "memory");  // the quantiser may stand by
     __shared__ int mine_of[kRouteWarps], below_of[kRouteWarps];
     const int e = blockIdx.x, warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
@@ -340,7 +335,6 @@ __global__ void __launch_bounds__(kRouteWarps * 32) k_mx_route(const int32_t* id
                     inv[q] = r++;
                 } else {
                     inv[q] = -1;
-                    for (int i = 0; i < N; ++i) y[(long long)q * N + i] = 0.0f;
                 }
             }
         }
@@ -414,10 +408,12 @@ __global__ void __launch_bounds__(256) k_mx_dequant(const uint8_t* codes, const 
     }
 }
 
+int cuts(int passes) { return passes < 65535 ? passes : 65535; }  // the grid's limit
+
 template <typename T>
 cudaError_t quant(const T* W, int N, int K, int rotate, uint8_t* codes, uint8_t* scales, cudaStream_t s) {
     const int blocks = (N + 127) / 128 * (128 / kRows), passes = (K / 128 + 4 * kWarps - 1) / (4 * kWarps);
-    const dim3 grid((unsigned)blocks, (unsigned)(blocks < 148 ? passes : 1));  // few rows: cut along K too
+    const dim3 grid((unsigned)blocks, (unsigned)(blocks < 148 ? cuts(passes) : 1));  // few rows: cut along K too
     k_mx_quant<T><<<grid, kWarps * 32, 0, s>>>(W, N, K, rotate, codes, scales);
     return cudaGetLastError();
 }
@@ -433,17 +429,17 @@ cudaError_t launch_mx_quant_rows(const void* x, int M, int K, int rotate, uint8_
     return quant(static_cast<const __nv_bfloat16*>(x), M, K, rotate, codes, scales, s);
 }
 
-cudaError_t launch_mx_route(const int32_t* ids, int P, int E, int32_t* offsets, int32_t* perm, int32_t* inv, float* y,
-                            int N, unsigned* err, cudaStream_t s) {
+cudaError_t launch_mx_route(const int32_t* ids, int P, int E, int32_t* offsets, int32_t* perm, int32_t* inv,
+                            unsigned* err, cudaStream_t s) {
     // Not as a dependent launch: its blocks, waiting beside the product before them, cost that 6 of 87 us.
-    k_mx_route<<<E + 1, kRouteWarps * 32, 0, s>>>(ids, P, E, offsets, perm, inv, y, N, err);
+    k_mx_route<<<E + 1, kRouteWarps * 32, 0, s>>>(ids, P, E, offsets, perm, inv, err);
     return cudaGetLastError();
 }
 
 cudaError_t launch_mx_act(const MxAct& a, cudaStream_t s) {
     // One CTA a row; few rows are cut along K instead, so that their columns are not walked one after another.
     const int rows = a.ids ? a.R / a.topk : a.R, passes = (a.K / 128 + 4 * kActWarps - 1) / (4 * kActWarps);
-    const dim3 grid((unsigned)rows, (unsigned)(rows < 148 ? passes : 1));
+    const dim3 grid((unsigned)rows, (unsigned)(rows < 148 ? cuts(passes) : 1));
     cudaLaunchConfig_t cfg = {};
     cfg.gridDim = grid;
     cfg.blockDim = dim3(kActWarps * 32);

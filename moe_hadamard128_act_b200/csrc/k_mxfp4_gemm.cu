@@ -360,19 +360,20 @@ constexpr int kPlanSms = 148;  // a plan goes by this GPU's count, so that a wor
 // 4-bit x, a round of 64, 96, 128, 160, 192, 208 and 256 operand rows takes 5.4, 6.1, 6.1, 7.0, 8.4, 8.8 and 9.9 us,
 // one of 16-bit parts the same in proportion.
 int pair_tokens(int P, long long R, int N, int experts) {
-    const long long wide = kMxRows / P, first = (R + wide - 1) / wide, blocks_n = (N + 2 * TM - 1) / (2 * TM);
-    long long best = 0, nt = 0;
-    for (long long b = first; b <= 4 * first + 8; ++b) {
-        const long long t = ((R + b - 1) / b + 15) / 16 * 16, rows = P * t;
-        if (nt && rows < 64) break;
+    const int wide = (int)min((R + 15) / 16 * 16, (long long)kMxRows / P);
+    const long long blocks_n = (N + 2 * TM - 1) / (2 * TM);
+    long long best = 0;
+    int nt = wide;
+    for (int t = wide; t == wide || P * t >= 64; t -= 16) {
+        const int rows = P * t;
         const long long tiles = blocks_n * experts * ((R + t - 1) / t), rounds = (tiles + kPlanSms / 2 - 1) / (kPlanSms / 2);
         const long long cost = rounds * (rows <= 128 ? 200 + rows * 2 / 5 : 150 + rows);
-        if (!nt || cost < best) {
+        if (t == wide || cost < best) {
             best = cost;
             nt = t;
         }
     }
-    return (int)nt;
+    return nt;
 }
 
 }  // namespace

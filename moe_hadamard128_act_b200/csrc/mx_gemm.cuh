@@ -182,8 +182,11 @@ __device__ __forceinline__ void route(const MxGemm& g, Routing& rt, int warp, in
     }
     __syncthreads();
     if (warp != 3) return;
+    // Sound segments make no more blocks than this.  Overlapping ones (offsets out of order) could make more tiles
+    // than a count holds: then there are none.
+    const int most = g.R / g.plan.nt + g.E;
     int sum = 0;
-    for (int e0 = 0; e0 < g.E; e0 += 32) {
+    for (int e0 = 0; e0 < g.E && sum <= most; e0 += 32) {
         const int v = e0 + lane < g.E ? cum[e0 + lane] : 0;
         int incl = v;
 #pragma unroll
@@ -193,6 +196,10 @@ __device__ __forceinline__ void route(const MxGemm& g, Routing& rt, int warp, in
         }
         if (e0 + lane < g.E) cum[e0 + lane] = sum + incl - v;
         sum += __shfl_sync(kFull, incl, 31);
+    }
+    if (sum > most) {
+        for (int e = lane; e < g.E; e += 32) cum[e] = 0;
+        sum = 0;
     }
     if (lane == 0) cum[g.E] = sum;
 }

@@ -268,7 +268,7 @@ int check_experts(const ql_experts* ex) {
     if (ex->fmt != QL_I8_G128_BF16 && ex->fmt != QL_I8_G128_F16 && ex->fmt != QL_FP8_B128_BF16 &&
         ex->fmt != QL_FP8A8_B128_BF16 && !fmt_mxfp4(ex->fmt))
         return QL_EUNSUPPORTED;
-    if (ex->K > QL_A16_MAX_K) return QL_EUNSUPPORTED;
+    if (!fmt_mxfp4(ex->fmt) && ex->K > QL_A16_MAX_K) return QL_EUNSUPPORTED;
     if (fmt_mxfp4(ex->fmt) && mx_too_many((long long)ex->E * ex->N)) return QL_EUNSUPPORTED;
     if (!ex->codes || !ex->scales) return QL_EINVAL;
     if (!aligned_codes(ex->fmt, ex->codes) || !aligned16(ex->scales)) return QL_EALIGN;
@@ -734,8 +734,8 @@ int moe_gate_up(const void* x, const int32_t* topk_ids, const float* topk_weight
         int32_t* const offsets = reinterpret_cast<int32_t*>(b + w.offsets);
         int32_t* const perm = reinterpret_cast<int32_t*>(b + w.perm);
         const int t = trace_begin(QL_KIND_MOE_PERMUTE, s);
-        e = launch_mx_route(topk_ids, R, experts->E, offsets, perm, reinterpret_cast<int32_t*>(b + w.inv), y,
-                            experts->N, di.err_word, s);
+        e = launch_mx_route(topk_ids, R, experts->E, offsets, perm, reinterpret_cast<int32_t*>(b + w.inv),
+                            di.err_word, s);
         trace_end(t, s);
         if (e != cudaSuccess) return from_cuda(e);
         return mx_product(x, experts->codes, experts->scales, experts->flags, R, experts->N, experts->K,

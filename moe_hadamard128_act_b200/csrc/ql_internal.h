@@ -272,15 +272,15 @@ struct MxAct {
     uint8_t* codes;   // E2M1 [R][K / 2], digits [8 R][K / 2], or E4M3 parts [2][R][K]
     uint8_t* scales;  // [slots][K / 128][nblk][512]
     float* factors;   // digits: what each sorted row's sums are to be multiplied by
-    float* y;         // plan.split: the rows' outputs, zeroed here
+    float* y;         // the rows' outputs, zeroed here with plan.split and for pairs of no expert
     int N;
     unsigned* err;
 };
 cudaError_t launch_mx_act(const MxAct& a, cudaStream_t s);
-// Sorted order of P routed pairs: offsets [E + 1], perm [P] (-1 past the routed ones), inv [P] (-1: of no expert; its
-// row of y [P][N] is zeroed and QL_DEVERR_EXPERT_ID set).
-cudaError_t launch_mx_route(const int32_t* ids, int P, int E, int32_t* offsets, int32_t* perm, int32_t* inv, float* y,
-                            int N, unsigned* err, cudaStream_t s);
+// Sorted order of P routed pairs: offsets [E + 1], perm [P] (-1 past the routed ones), inv [P] (-1: of no expert, and
+// QL_DEVERR_EXPERT_ID set).
+cudaError_t launch_mx_route(const int32_t* ids, int P, int E, int32_t* offsets, int32_t* perm, int32_t* inv,
+                            unsigned* err, cudaStream_t s);
 struct MxGemm {
     const uint8_t* codes;   // [E][N][K / 2]
     const uint8_t* scales;  // [E][ceil(N / 128)][K / 128][512]

@@ -434,3 +434,63 @@ def test_side_stream_and_graphs_that_share_a_workspace(Q, fmt):
         torch.cuda.synchronize()
         for b, y in zip(new, ys):
             close(y, *X.forward(b, W, fmt))
+
+
+@pytest.mark.parametrize("fmt", FMTS)
+def test_grouped_many_overlapping_segments(Q, fmt):
+    # every second expert claims every row: flagged, and nothing outside y is touched
+    E, N, K, R = 64, 130, 128, 600
+    c, s, _ = weight(Q, N, K)
+    y = torch.full((R + 1, N), 7.0, device="cuda")
+    offsets = np.array([0, R] * (E // 2) + [0], np.int32)
+    Q.qlinear_grouped(dev_bf16(x_bits(R, K)), dev(offsets), c.repeat(E), s.repeat(E), E, N, fmt, y=y[:R])
+    assert Q.ql_get_device_error() == (6, Q.DEVERR_BOUNDS)
+    assert (y[R] == 7.0).all()
+
+
+@pytest.mark.parametrize("fmt", FMTS)
+def test_grouped_and_gate_up_of_long_rows(Q, fmt):
+    E, N, K, R = 2, 40, 32896, 5
+    x, offsets = x_bits(R, K), [0, 2, 5]
+    c, s, W = weight(Q, N, K)
+    got = Q.qlinear_grouped(dev_bf16(x), dev(np.array(offsets, np.int32)), c.repeat(E), s.repeat(E), E, N, fmt)
+    close(got, *X.forward(x, W, fmt))
+    ids = dev(np.arange(R, dtype=np.int32).reshape(R, 1) % E)
+    close(Q.moe_gate_up(dev_bf16(x), ids, c.repeat(E), s.repeat(E), E, N, fmt=fmt, flags=0)[:, 0], *X.forward(x, W, fmt))
+
+
+@pytest.mark.parametrize("fmt", FMTS)
+def test_gate_up_most_pairs_of_no_expert(Q, fmt):
+    T, topk, E, N, K = 500, 4, 8, 260, 256
+    ids = np.full((T, topk), -1, np.int32)
+    ids[::50, 2] = 5
+    x = x_bits(T, K)
+    c, s, W = weight(Q, N, K)
+    y = torch.full((T, topk, N), float("nan"), device="cuda")
+    Q.moe_gate_up(dev_bf16(x), dev(ids), c.repeat(E), s.repeat(E), E, N, fmt=fmt, flags=0, y=y)
+    assert Q.ql_get_device_error() == (6, Q.DEVERR_EXPERT_ID)
+    close(y[::50, 2], *X.forward(x[::50], W, fmt))
+    y[::50, 2] = 0
+    assert not y.any()
+
+
+@pytest.mark.parametrize("fmt", FMTS)
+def test_stream_argument_owns_what_the_call_allocates(Q, fmt):
+    # memory that the call took on a busy side stream is not handed to the current stream when the call returns
+    N, K, M = 300, 1024, 40
+    x = x_bits(M, K)
+    c, s, W = weight(Q, N, K)
+    side, xd = torch.cuda.Stream(), dev_bf16(x)
+    need = Q.qlinear_workspace_size(fmt, 0, M, N, K)
+    torch.cuda.synchronize()
+    with torch.cuda.stream(side):
+        torch.cuda._sleep(20_000_000)
+    y = Q.qlinear_forward(xd, c, s, None, fmt, N, stream=side)
+    codes, scales = Q.act_quant_mxfp4(xd, stream=side)
+    for _ in range(4):
+        torch.empty(need, dtype=torch.uint8, device="cuda").fill_(0xFF)
+    torch.cuda.synchronize()
+    close(y, *X.forward(x, W, fmt))
+    n, b = X.quantise(O.bf16_decode(x.ravel()).reshape(M, K))
+    rc, rs = X.pack(n, b)
+    assert np.array_equal(host_u8(codes).ravel(), rc.ravel()) and np.array_equal(host_u8(scales).ravel(), rs.ravel())
