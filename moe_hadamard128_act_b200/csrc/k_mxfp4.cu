@@ -185,8 +185,8 @@ __global__ void __launch_bounds__(kActWarps * 32) k_mx_act(const MxAct a) {
     }
     __syncthreads();
     for (int j = 0; j < dests; ++j) {
-        // Zeroed: rows that the product adds into, and those of pairs that no expert takes.
-        if (places[j].row < 0 ? !a.ids : !a.plan.split) continue;
+        // Zeroed: what the product adds into, and the rows of pairs that no expert takes.
+        if (places[j].row < 0 ? !a.ids : !(a.plan.split | a.plan.halves)) continue;
         float* const y = places[j].y;
         for (int n = blockIdx.y * blockDim.x + threadIdx.x; n < a.N; n += gridDim.y * blockDim.x) y[n] = 0.0f;
     }

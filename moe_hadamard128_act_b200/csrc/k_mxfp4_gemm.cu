@@ -355,22 +355,34 @@ namespace {
 
 constexpr int kPlanSms = 148;  // a plan goes by this GPU's count, so that a workspace size does not depend on a device
 
-// Tokens of a block for `experts` weights of R rows each on pairs of CTAs: the cut with the least rounds of tiles
-// times what a tile of so many operand rows takes.  Measured at 5376 columns, 74 x 256 weight rows and 2048 rows of
-// 4-bit x, a round of 64, 96, 128, 160, 192, 208 and 256 operand rows takes 5.4, 6.1, 6.1, 7.0, 8.4, 8.8 and 9.9 us,
-// one of 16-bit parts the same in proportion.
-int pair_tokens(int P, long long R, int N, int experts) {
+constexpr int kPairs = kPlanSms / 2;
+
+// Tokens of a block for weights of R rows each on pairs of CTAs, and whether its tiles are halved along K: the cut with
+// the least rounds of tiles times what a tile of so many operand rows takes.  Measured at 5376 columns, 74 x 256 weight
+// rows and 2048 rows of 4-bit x, a round of 64, 96, 128, 160, 192, 208 and 256 operand rows takes 5.4, 6.1, 6.1, 7.0,
+// 8.4, 8.8 and 9.9 us, one of 16-bit parts half as much again, but no less than the spreading copies' 9.4.
+// Tiles of one weight that leave half of the pairs without work may be halved, which costs zeroed outputs and adding
+// into them, 2 us and half a us for every MB: 5376 x 21504 at 128 rows takes 23.3 us against 29.4 (4-bit x) and 38.9
+// against 50.0 (parts), but 4096 x 4096 at 256 rows 15.3 against 12.8.
+int pair_tokens(int P, long long R, int N, int K, int E, int* halves) {
     const int wide = (int)min((R + 15) / 16 * 16, (long long)kMxRows / P);
-    const long long blocks_n = (N + 2 * TM - 1) / (2 * TM);
-    long long best = 0;
+    const long long blocks_n = (N + 2 * TM - 1) / (2 * TM) * (long long)(E ? E : 1);
+    double best = 0;
     int nt = wide;
+    *halves = 0;
     for (int t = wide; t == wide || P * t >= 64; t -= 16) {
         const int rows = P * t;
-        const long long tiles = blocks_n * experts * ((R + t - 1) / t), rounds = (tiles + kPlanSms / 2 - 1) / (kPlanSms / 2);
-        const long long cost = rounds * (rows <= 128 ? 200 + rows * 2 / 5 : 150 + rows);
+        const long long tiles = blocks_n * ((R + t - 1) / t), rounds = (tiles + kPairs - 1) / kPairs;
+        double tile = rows <= 128 ? 4.9 + rows * 0.01 : 3.7 + rows * 0.0244;
+        if (P > 1) tile = 1.5 * tile > 9.4 ? 1.5 * tile : 9.4;
+        tile *= K / 5376.0;
+        const double half = tile / 2 + 2 + 0.5e-6 * 4 * R * N;
+        const bool cut = E == 0 && 2 * tiles <= kPairs && K >= 512 && half < tile;
+        const double cost = cut ? half : rounds * tile;
         if (t == wide || cost < best) {
             best = cost;
             nt = t;
+            *halves = cut;
         }
     }
     return nt;
@@ -378,8 +390,9 @@ int pair_tokens(int P, long long R, int N, int experts) {
 
 }  // namespace
 
-MxPlan mx_plan(bool a16, int R, int N, int E) {
+MxPlan mx_plan(bool a16, int R, int N, int K, int E) {
     MxPlan p;
+    p.halves = 0;
     const long long per = E ? ((long long)R + E - 1) / E : R;  // rows an expert
     // Digits up to two blocks of one weight (21504 x 5376 at 32 rows 24.9 us against 26.5, at 48 rows 27.1 against
     // 28.6, at 64 rows parts take 27.3), or 20 rows an expert (128 of 1408 x 2816 at 280 tokens 70.6 against 76.7, at
@@ -403,8 +416,9 @@ MxPlan mx_plan(bool a16, int R, int N, int E) {
     } else {
         // Pairs once a token block is wide enough for its operand stream to count: 21504 x 5376 at 64 rows 20.5 us
         // against 22.3, at 192 rows 27.1 against 30.6.
-        p.nt = pair_tokens(P, per, N, E ? E : 1);
+        p.nt = pair_tokens(P, per, N, K, E, &p.halves);
         p.pair = P * p.nt >= 64;
+        p.halves &= p.pair;
     }
     p.nblk = (P * p.nt + 127) / 128;
     // Cutting tiles along K costs a zeroed y: worth it while y is small beside the weights.

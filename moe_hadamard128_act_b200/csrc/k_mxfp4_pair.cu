@@ -22,6 +22,10 @@
 // operand bytes a product, fills half of the tensor memory with one: its epilogue
 // takes the sums into registers, gives the accumulator back and then stores.
 //
+// A weight whose tiles would leave half of the pairs idle may have each cut in half along K between two pairs
+// (MxPlan::halves); as in k_mxfp4_gemm.cu both add into zeroed outputs, in either order.  The epilogue's two forms are
+// apart because one that decides for every output costs 128 experts at 2048 tokens 103 us instead of 88.
+//
 // Waits are bounded as in k_mxfp4_gemm.cu; a CTA that gave up stays until copies
 // that it started have landed, and both CTAs leave together.
 #include "mx_gemm.cuh"
@@ -174,7 +178,7 @@ __global__ void __launch_bounds__(kThreads, 1) k_mx_pair(const __grid_constant__
             // Past the last row of all (an odd number of 128-row blocks) the scales are some block's: no output
             // comes of those rows.
             const int sf = (e * NB + min(wb, NB - 1)) * G;
-            for (int k = 0; k < KS; ++k) {
+            for (int k = uniform(ti.k0), k1 = uniform(ti.k1); k < k1; ++k) {
                 if (!__all_sync(kFull, mbar_wait(bar(B_EMPTY + s), ph, lim))) {
                     dead = true;
                     break;
@@ -199,7 +203,7 @@ __global__ void __launch_bounds__(kThreads, 1) k_mx_pair(const __grid_constant__
             const int half = uniform(PARTS ? mx_pad16(ti.rows) : ((ti.rows + 31) & ~31) / 2);
             const int row = PARTS ? rank * g.R + uniform(ti.row0) : uniform(ti.row0) + rank * half;
             const int sf = uniform(ti.slot) * G * nblk;
-            for (int k = 0; k < KS; ++k) {
+            for (int k = uniform(ti.k0), k1 = uniform(ti.k1); k < k1; ++k) {
                 if (!__all_sync(kFull, mbar_wait(bar(B_EMPTY + s), ph, lim))) {
                     dead = true;
                     break;
@@ -223,7 +227,7 @@ __global__ void __launch_bounds__(kThreads, 1) k_mx_pair(const __grid_constant__
         int os = 0, oph = 0;       // ring slot (and its phase) of the step that had them before
         long long step = 0;
         while (!dead && tiles.next(ti)) {
-            for (int k = 0; k < KS; ++k, ++step) {
+            for (int k = uniform(ti.k0), k1 = uniform(ti.k1); k < k1; ++k, ++step) {
                 bool ok = pair_wait(bar(B_FULL + s), ph, lim);
                 // The MMAs that read these columns before are done: the load that filled the slot waited for them
                 // if there are as many columns as slots.
@@ -268,7 +272,8 @@ __global__ void __launch_bounds__(kThreads, 1) k_mx_pair(const __grid_constant__
             }
             const int cols = uniform(PARTS ? 2 * mx_pad16(ti.rows) : (ti.rows + 31) & ~31);
             const uint32_t d = tmem + b * p.acc_cols, id0 = idesc<MODE>(PM, cols);
-            for (int k = 0; k < KS; ++k) {
+            const int k0 = uniform(ti.k0), k1 = uniform(ti.k1);
+            for (int k = k0; k < k1; ++k) {
                 // the scales are in place, and with them the operands, which their copier waited for
                 if (!__all_sync(kFull, mbar_wait(bar(B_SF + q), qph, lim))) {
                     dead = true;
@@ -285,7 +290,7 @@ __global__ void __launch_bounds__(kThreads, 1) k_mx_pair(const __grid_constant__
                         const int i = PARTS ? 0 : j >> 1, byte = PARTS ? j : 2 * (j & 1);  // its scales' block and byte
                         if (i < kbs)
                             pair_mma<MODE>(d, ad + 2 * j, bd + 2 * j, id0 | (uint32_t)byte << 4 | (uint32_t)byte << 29,
-                                           sf + 4 * i, sfb + 4 * nblk * i, (k | j) ? 1u : 0u);
+                                           sf + 4 * i, sfb + 4 * nblk * i, (k > k0 || j) ? 1u : 0u);
                     }
                     pair_commit(bar(B_EMPTY + s));  // both CTAs' slots may be refilled once these are done
                 }
@@ -319,7 +324,9 @@ __global__ void __launch_bounds__(kThreads, 1) k_mx_pair(const __grid_constant__
             fence_before();
             __syncwarp();
             if (lane == 0) pair_arrive(in_even(bar(B_ACCE + b)));
-            epi.store(g, ti, h, (2 * ti.wb + rank) * TM + 32 * q + lane, false);
+            const int n = (2 * ti.wb + rank) * TM + 32 * q + lane;
+            if (ti.k1 - ti.k0 == KS) epi.store(g, ti, h, n, false);
+            else epi.store(g, ti, h, n, true);
             ++tl;
         }
     }
@@ -398,7 +405,8 @@ cudaError_t run(const MxGemm& g, cudaStream_t s) {
         if (pairs < 1) return cudaErrorInvalidValue;
         if (dev < 64) pairs_of[dev] = pairs;
     }
-    const long long tiles = (long long)((g.N + PM - 1) / PM) * mx_slots(g.R, g.offsets || g.ids ? g.E : 0, g.plan.nt);
+    long long tiles = (long long)((g.N + PM - 1) / PM) * mx_slots(g.R, g.offsets || g.ids ? g.E : 0, g.plan.nt);
+    if (g.plan.halves) tiles *= 2;
     cfg.gridDim = dim3((unsigned)(2 * (tiles < pairs ? tiles : pairs)));
     cfg.numAttrs = 2;
     e = cudaLaunchKernelEx(&cfg, k_mx_pair<MODE>, p);

@@ -169,7 +169,7 @@ struct MxWs {
 };
 MxWs mx_ws(int fmt, int R, int N, int K, int E, bool pairs) {
     MxWs w;
-    w.plan = mx_plan(fmt == QL_MXFP4_G32, R, N, E);
+    w.plan = mx_plan(fmt == QL_MXFP4_G32, R, N, K, E);
     const size_t row = w.plan.mode == kMxA4 ? K / 2 : w.plan.mode == kMxDigits ? (size_t)4 * K : (size_t)2 * K;
     size_t o = 0;
     w.xq = o; o += align_up((size_t)R * row, 256);

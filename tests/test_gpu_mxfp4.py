@@ -494,3 +494,17 @@ def test_stream_argument_owns_what_the_call_allocates(Q, fmt):
     n, b = X.quantise(O.bf16_decode(x.ravel()).reshape(M, K))
     rc, rs = X.pack(n, b)
     assert np.array_equal(host_u8(codes).ravel(), rc.ravel()) and np.array_equal(host_u8(scales).ravel(), rs.ravel())
+
+
+@pytest.mark.parametrize("fmt", FMTS)
+@pytest.mark.parametrize("M,N,K,had", [(65, 300, 2048, 0), (100, 1000, 2176, 1), (130, 2600, 2304, 0), (200, 520, 4224, 0),
+                                       (300, 6500, 2048, 0), (700, 5130, 2176, 0)])
+def test_forward_last_tiles_cut_along_k(Q, fmt, M, N, K, had):
+    x = x_bits(M, K, seed=4)
+    c, s, W = weight(Q, N, K, seed=4)
+    xd = dev_bf16(x)
+    y = torch.full((M, N), float("nan"), device="cuda")
+    Q.qlinear_forward(xd, c, s, None, fmt, N, flags=had, y=y)
+    close(y, *X.forward(x, W, fmt, bool(had)))
+    for _ in range(5):
+        assert torch.equal(Q.qlinear_forward(xd, c, s, None, fmt, N, flags=had), y)
