@@ -83,7 +83,9 @@ __device__ __forceinline__ void commit(uint32_t bar) {
     asm volatile("tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0];\n" ::"r"(bar)
                  : "memory");
 }
-template <int MODE>
+// ROWS: operand rows of a block at most.  The epilogue is written out for them, and a decode call waits for the
+// instructions of a long one.
+template <int MODE, int ROWS>
 __global__ void __launch_bounds__(kThreads, 1) k_mx_gemm(const __grid_constant__ MxParams p) {
     extern __shared__ uint8_t smem_raw[];
     __shared__ __align__(8) uint64_t bars[NBARS];
@@ -271,7 +273,7 @@ __global__ void __launch_bounds__(kThreads, 1) k_mx_gemm(const __grid_constant__
         int tl = 0;
         while (tiles.next(ti)) {
             const int b = tl & 1;
-            Epilogue<MODE> epi;
+            Epilogue<MODE, ROWS> epi;
             epi.fetch(g, rt, ti, h, lane);
             if (!__all_sync(kFull, mbar_wait(bar(B_ACCF + b), (tl >> 1) & 1, lim))) {  // together
                 dead = true;
@@ -296,7 +298,7 @@ __global__ void __launch_bounds__(kThreads, 1) k_mx_gemm(const __grid_constant__
     }
 }
 
-template <int MODE>
+template <int MODE, int ROWS>
 cudaError_t run(const MxGemm& g, cudaStream_t s) {
     DeviceInfo di;
     cudaError_t e = device_info(&di);
@@ -306,6 +308,7 @@ cudaError_t run(const MxGemm& g, cudaStream_t s) {
     MxParams p;
     p.g = g;
     const int nblk = g.plan.nblk, rows = P * g.plan.nt;  // operand rows of a full token block
+    if (rows > ROWS) return cudaErrorInvalidValue;
     p.stage_bytes = (int)align_up(A_BYTES + rows * 128 + KBS * (1 + nblk) * 512, 1024);
     p.acc_cols = (int)align_up(rows, 32);
     p.sf0 = 2 * p.acc_cols;
@@ -329,7 +332,7 @@ cudaError_t run(const MxGemm& g, cudaStream_t s) {
     int dev = 0;
     cudaGetDevice(&dev);
     if (dev >= 64 || !attr_set[dev]) {
-        e = cudaFuncSetAttribute(k_mx_gemm<MODE>, cudaFuncAttributeMaxDynamicSharedMemorySize, kSmemMax);
+        e = cudaFuncSetAttribute(k_mx_gemm<MODE, ROWS>, cudaFuncAttributeMaxDynamicSharedMemorySize, kSmemMax);
         if (e != cudaSuccess) return e;
         if (dev < 64) attr_set[dev] = true;
     }
@@ -345,7 +348,7 @@ cudaError_t run(const MxGemm& g, cudaStream_t s) {
     attr[0].val.programmaticStreamSerializationAllowed = 1;  // after this library's quantiser
     cfg.attrs = attr;
     cfg.numAttrs = 1;
-    e = cudaLaunchKernelEx(&cfg, k_mx_gemm<MODE>, p);
+    e = cudaLaunchKernelEx(&cfg, k_mx_gemm<MODE, ROWS>, p);
     return e != cudaSuccess ? e : cudaGetLastError();
 }
 
@@ -430,9 +433,9 @@ MxPlan mx_plan(bool a16, int R, int N, int K, int E) {
 cudaError_t launch_mx_gemm(const MxGemm& g, cudaStream_t s) {
     if (g.plan.pair) return launch_mx_pair(g, s);
     switch (g.plan.mode) {
-    case kMxA4: return run<kMxA4>(g, s);
-    case kMxDigits: return run<kMxDigits>(g, s);
-    default: return run<kMxParts>(g, s);
+    case kMxA4: return g.plan.nt <= 64 ? run<kMxA4, 64>(g, s) : run<kMxA4, kMxRows2>(g, s);
+    case kMxDigits: return run<kMxDigits, kMxRows2>(g, s);
+    default: return run<kMxParts, 64>(g, s);  // wider ones go to pairs
     }
 }
 

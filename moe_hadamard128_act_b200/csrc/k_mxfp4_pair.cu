@@ -313,7 +313,7 @@ __global__ void __launch_bounds__(kThreads, 1) k_mx_pair(const __grid_constant__
         int tl = 0;
         while (tiles.next(ti)) {
             const int b = p.nacc == 2 ? tl & 1 : 0, use = p.nacc == 2 ? tl >> 1 : tl;
-            Epilogue<MODE> epi;
+            Epilogue<MODE, kMxRows> epi;
             epi.fetch(g, rt, ti, h, lane);
             if (!__all_sync(kFull, mbar_wait(bar(B_ACCF + b), use & 1, lim))) {  // together
                 dead = true;

@@ -214,12 +214,12 @@ __device__ __forceinline__ void route(const MxGemm& g, Routing& rt, int warp, in
 
 // The epilogue of one tile in two halves, for warp kEpiWarp0 + w: lanes 32 (w % 4) .. + 31 of the accumulator are
 // weight rows, i.e. consecutive outputs of a token; the two warps of a lane quarter take every second read.
-template <int MODE>
+// ROWS: operand rows of a block at most.
+template <int MODE, int ROWS>
 struct Epilogue {
     static constexpr bool PARTS = MODE == kMxParts;
     static constexpr int TW = MODE == kMxDigits ? CW / 8 : CW;        // tokens of a tensor-memory read
-    // this warp's reads (16-bit activations: a block has no more than kMxRows2 operand rows in digits)
-    static constexpr int READS = (MODE == kMxDigits ? kMxRows2 : kMxRows) / mx_planes(MODE) / TW / 2;
+    static constexpr int READS = ROWS / mx_planes(MODE) / TW / 2;     // this warp's
     static constexpr int REGS = (READS * TW + 31) / 32;
     int to[REGS];
     float factor[REGS];
