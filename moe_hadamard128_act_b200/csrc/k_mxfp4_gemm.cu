@@ -434,7 +434,7 @@ cudaError_t launch_mx_gemm(const MxGemm& g, cudaStream_t s) {
     if (g.plan.pair) return launch_mx_pair(g, s);
     switch (g.plan.mode) {
     case kMxA4: return g.plan.nt <= 64 ? run<kMxA4, 64>(g, s) : run<kMxA4, kMxRows2>(g, s);
-    case kMxDigits: return run<kMxDigits, kMxRows2>(g, s);
+    case kMxDigits: return g.plan.nt <= 8 ? run<kMxDigits, 64>(g, s) : run<kMxDigits, kMxRows2>(g, s);
     default: return run<kMxParts, 64>(g, s);  // wider ones go to pairs
     }
 }

@@ -120,7 +120,7 @@ __device__ __forceinline__ void pair_arrive(uint32_t cluster_bar) {
     asm volatile("mbarrier.arrive.release.cluster.shared::cluster.b64 _, [%0];\n" ::"r"(cluster_bar) : "memory");
 }
 
-template <int MODE>
+template <int MODE, int ROWS>  // ROWS: operand rows of a block at most
 __global__ void __launch_bounds__(kThreads, 1) k_mx_pair(const __grid_constant__ PairParams p) {
     extern __shared__ uint8_t smem_raw[];
     __shared__ __align__(8) uint64_t bars[NBARS];
@@ -313,7 +313,7 @@ __global__ void __launch_bounds__(kThreads, 1) k_mx_pair(const __grid_constant__
         int tl = 0;
         while (tiles.next(ti)) {
             const int b = p.nacc == 2 ? tl & 1 : 0, use = p.nacc == 2 ? tl >> 1 : tl;
-            Epilogue<MODE, kMxRows> epi;
+            Epilogue<MODE, ROWS> epi;
             epi.fetch(g, rt, ti, h, lane);
             if (!__all_sync(kFull, mbar_wait(bar(B_ACCF + b), use & 1, lim))) {  // together
                 dead = true;
@@ -348,7 +348,7 @@ __global__ void __launch_bounds__(kThreads, 1) k_mx_pair(const __grid_constant__
     }
 }
 
-template <int MODE>
+template <int MODE, int ROWS>
 cudaError_t run(const MxGemm& g, cudaStream_t s) {
     DeviceInfo di;
     cudaError_t e = device_info(&di);
@@ -359,6 +359,7 @@ cudaError_t run(const MxGemm& g, cudaStream_t s) {
     PairParams p;
     p.g = g;
     const int nblk = g.plan.nblk, rows = (P * g.plan.nt + 31) / 32 * 32;  // operand rows of a full token block
+    if (rows > ROWS) return cudaErrorInvalidValue;
     p.stage_bytes = (int)align_up(A_BYTES + rows / 2 * 128 + KBS * (1 + nblk) * 512, 1024);
     p.acc_cols = rows;
     p.nacc = rows <= kMxRows2 ? 2 : 1;
@@ -395,11 +396,11 @@ cudaError_t run(const MxGemm& g, cudaStream_t s) {
     cfg.attrs = attr;
     int pairs = dev < 64 ? pairs_of[dev] : 0;
     if (!pairs) {
-        e = cudaFuncSetAttribute(k_mx_pair<MODE>, cudaFuncAttributeMaxDynamicSharedMemorySize, kSmemMax);
+        e = cudaFuncSetAttribute(k_mx_pair<MODE, ROWS>, cudaFuncAttributeMaxDynamicSharedMemorySize, kSmemMax);
         if (e != cudaSuccess) return e;
         cfg.gridDim = dim3(di.sm_count / 2 * 2);
         cfg.numAttrs = 1;
-        e = cudaOccupancyMaxActiveClusters(&pairs, k_mx_pair<MODE>, &cfg);
+        e = cudaOccupancyMaxActiveClusters(&pairs, k_mx_pair<MODE, ROWS>, &cfg);
         if (e != cudaSuccess) return e;
         if (pairs > di.sm_count / 2) pairs = di.sm_count / 2;
         if (pairs < 1) return cudaErrorInvalidValue;
@@ -409,14 +410,16 @@ cudaError_t run(const MxGemm& g, cudaStream_t s) {
     if (g.plan.halves) tiles *= 2;
     cfg.gridDim = dim3((unsigned)(2 * (tiles < pairs ? tiles : pairs)));
     cfg.numAttrs = 2;
-    e = cudaLaunchKernelEx(&cfg, k_mx_pair<MODE>, p);
+    e = cudaLaunchKernelEx(&cfg, k_mx_pair<MODE, ROWS>, p);
     return e != cudaSuccess ? e : cudaGetLastError();
 }
 
 }  // namespace
 
 cudaError_t launch_mx_pair(const MxGemm& g, cudaStream_t s) {
-    return g.plan.mode == kMxParts ? run<kMxParts>(g, s) : run<kMxA4>(g, s);
+    const bool wide = mx_planes(g.plan.mode) * g.plan.nt > 128;
+    if (g.plan.mode == kMxParts) return wide ? run<kMxParts, kMxRows>(g, s) : run<kMxParts, 128>(g, s);
+    return wide ? run<kMxA4, kMxRows>(g, s) : run<kMxA4, 128>(g, s);
 }
 
 }  // namespace ql
