@@ -186,9 +186,10 @@ __global__ void __launch_bounds__(kActWarps * 32) k_mx_act(const MxAct a) {
     __syncthreads();
     for (int j = 0; j < dests; ++j) {
         // Zeroed: what the product adds into, and the rows of pairs that no expert takes.
-        if (places[j].row < 0 ? !a.ids : !(a.plan.split | a.plan.halves)) continue;
+        const bool none = places[j].row < 0;
+        if (none && !a.ids) continue;
         float* const y = places[j].y;
-        for (int n = blockIdx.y * blockDim.x + threadIdx.x; n < a.N; n += gridDim.y * blockDim.x) y[n] = 0.0f;
+        for (int n = (none ? 0 : a.plan.zero) + blockIdx.y * blockDim.x + threadIdx.x; n < a.N; n += gridDim.y * blockDim.x) y[n] = 0.0f;
     }
     if (dests == 1 && places[0].row < 0) return;
     while (g0 < G) {

@@ -360,32 +360,34 @@ constexpr int kPlanSms = 148;  // a plan goes by this GPU's count, so that a wor
 
 constexpr int kPairs = kPlanSms / 2;
 
-// Tokens of a block for weights of R rows each on pairs of CTAs, and whether its tiles are halved along K: the cut with
-// the least rounds of tiles times what a tile of so many operand rows takes.  Measured at 5376 columns, 74 x 256 weight
-// rows and 2048 rows of 4-bit x, a round of 64, 96, 128, 160, 192, 208 and 256 operand rows takes 5.4, 6.1, 6.1, 7.0,
-// 8.4, 8.8 and 9.9 us, one of 16-bit parts half as much again, but no less than the spreading copies' 9.4.
-// Tiles of one weight that leave half of the pairs without work may be halved, which costs zeroed outputs and adding
-// into them, 2 us and half a us for every MB: 5376 x 21504 at 128 rows takes 23.3 us against 29.4 (4-bit x) and 38.9
-// against 50.0 (parts), but 4096 x 4096 at 256 rows 15.3 against 12.8.
-int pair_tokens(int P, long long R, int N, int K, int E, int* halves) {
+// Tokens of a block for weights of R rows each on pairs of CTAs, and how many of its tiles, the last ones, are halved
+// along K: the cut with the least rounds of tiles times what a tile of so many operand rows takes.  Measured at 5376
+// columns, 74 x 256 weight rows and 2048 rows of 4-bit x, a round of 64, 96, 128, 160, 192, 208 and 256 operand rows
+// takes 5.4, 6.1, 6.1, 7.0, 8.4, 8.8 and 9.9 us, one of 16-bit parts half as much again, but no less than the spreading
+// copies' 9.4.
+// Halves, of one weight's tiles that leave half of the pairs without work, cost zeroed outputs and adding into them, 2 us
+// and half a us for every MB: 5376 x 21504 at 128 rows takes 22.9 us with them and 29.3 without (4-bit x) and 38.9
+// against 49.4 (parts), but 4096 x 4096 at 256 rows 15.3 against 12.8.  After full rounds only parts gain (21504 x 5376
+// at 96 rows 28.5 against 32.3): 4-bit x finds more bandwidth in a round that is not full and takes 22.6 against 21.3.
+int pair_tokens(int P, long long R, int N, int K, int E, int* halved) {
     const int wide = (int)min((R + 15) / 16 * 16, (long long)kMxRows / P);
     const long long blocks_n = (N + 2 * TM - 1) / (2 * TM) * (long long)(E ? E : 1);
     double best = 0;
     int nt = wide;
-    *halves = 0;
+    *halved = 0;
     for (int t = wide; t == wide || P * t >= 64; t -= 16) {
         const int rows = P * t;
-        const long long tiles = blocks_n * ((R + t - 1) / t), rounds = (tiles + kPairs - 1) / kPairs;
+        const long long tiles = blocks_n * ((R + t - 1) / t), full = tiles / kPairs, tail = tiles % kPairs;
         double tile = rows <= 128 ? 4.9 + rows * 0.01 : 3.7 + rows * 0.0244;
         if (P > 1) tile = 1.5 * tile > 9.4 ? 1.5 * tile : 9.4;
         tile *= K / 5376.0;
-        const double half = tile / 2 + 2 + 0.5e-6 * 4 * R * N;
-        const bool cut = E == 0 && 2 * tiles <= kPairs && K >= 512 && half < tile;
-        const double cost = cut ? half : rounds * tile;
+        const double half = tile / 2 + 2 + 0.5e-6 * 4 * (2 * TM) * t * tail;
+        const bool cut = E == 0 && 2 * tail <= kPairs && (P > 1 || full == 0) && K >= 512 && half < tile;
+        const double cost = full * tile + (tail == 0 ? 0 : cut ? half : tile);
         if (t == wide || cost < best) {
             best = cost;
             nt = t;
-            *halves = cut;
+            *halved = cut ? (int)tail : 0;
         }
     }
     return nt;
@@ -395,7 +397,7 @@ int pair_tokens(int P, long long R, int N, int K, int E, int* halves) {
 
 MxPlan mx_plan(bool a16, int R, int N, int K, int E) {
     MxPlan p;
-    p.halves = 0;
+    int halved = 0;
     const long long per = E ? ((long long)R + E - 1) / E : R;  // rows an expert
     // Digits up to two blocks of one weight (21504 x 5376 at 32 rows 24.9 us against 26.5, at 48 rows 27.1 against
     // 28.6, at 64 rows parts take 27.3), or 20 rows an expert (128 of 1408 x 2816 at 280 tokens 70.6 against 76.7, at
@@ -419,14 +421,20 @@ MxPlan mx_plan(bool a16, int R, int N, int K, int E) {
     } else {
         // Pairs once a token block is wide enough for its operand stream to count: 21504 x 5376 at 64 rows 20.5 us
         // against 22.3, at 192 rows 27.1 against 30.6.
-        p.nt = pair_tokens(P, per, N, K, E, &p.halves);
+        p.nt = pair_tokens(P, per, N, K, E, &halved);
         p.pair = P * p.nt >= 64;
-        p.halves &= p.pair;
     }
     p.nblk = (P * p.nt + 127) / 128;
     // Cutting tiles along K costs a zeroed y: worth it while y is small beside the weights.
     const long long tiles = (long long)((N + TM - 1) / TM) * mx_slots(R, 0, p.nt);
     p.split = !p.pair && (long long)R * N * 4 <= (4 << 20) && (E || tiles < 8LL * kPlanSms);
+    p.zero = p.split ? 0 : N;
+    p.halves = INT_MAX;
+    if (p.pair && halved) {
+        const long long nb = mx_slots(R, 0, p.nt);
+        p.halves = (int)((N + 2 * TM - 1) / (2 * TM) * nb - halved);
+        p.zero = (int)min(p.halves / nb * (2 * TM), (long long)N);
+    }
     return p;
 }
 

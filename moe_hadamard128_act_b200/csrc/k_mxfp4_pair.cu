@@ -22,8 +22,8 @@
 // operand bytes a product, fills half of the tensor memory with one: its epilogue
 // takes the sums into registers, gives the accumulator back and then stores.
 //
-// A weight whose tiles would leave half of the pairs idle may have each cut in half along K between two pairs
-// (MxPlan::halves); as in k_mxfp4_gemm.cu both add into zeroed outputs, in either order.  The epilogue's two forms are
+// The tiles of one weight's last round, if they would leave half of the pairs idle, may be cut in half along K between
+// two pairs each (MxPlan::halves); as in k_mxfp4_gemm.cu both add into zeroed outputs, in either order.  The epilogue's two forms are
 // apart because one that decides for every output costs 128 experts at 2048 tokens 103 us instead of 88.
 //
 // Waits are bounded as in k_mxfp4_gemm.cu; a CTA that gave up stays until copies
@@ -407,7 +407,7 @@ cudaError_t run(const MxGemm& g, cudaStream_t s) {
         if (dev < 64) pairs_of[dev] = pairs;
     }
     long long tiles = (long long)((g.N + PM - 1) / PM) * mx_slots(g.R, g.offsets || g.ids ? g.E : 0, g.plan.nt);
-    if (g.plan.halves) tiles *= 2;
+    if (tiles > g.plan.halves) tiles += tiles - g.plan.halves;
     cfg.gridDim = dim3((unsigned)(2 * (tiles < pairs ? tiles : pairs)));
     cfg.numAttrs = 2;
     e = cudaLaunchKernelEx(&cfg, k_mx_pair<MODE, ROWS>, p);

@@ -86,18 +86,21 @@ __device__ __forceinline__ void segment(const MxGemm& g, const Routing& rt, int 
 
 // The tiles of unit `id` of `units` (a CTA, or a pair of them), each role walking the same list: weight block (of
 // TR rows) by weight block within an expert so that its token blocks share the weights in L2.  With `split` tiles may be
-// cut along K between two units.  Pairs cut all tiles in half along K or none (g.plan.halves).
+// cut along K between two units.  Pairs cut those from g.plan.halves on in half along K.
 template <int TR>
 struct Tiles {
     static constexpr bool PAIR = TR > TM;
     const MxGemm& g;
     const Routing& rt;
-    int NB, KS, units, total, t;
+    int NB, KS, units, total, t, whole;  // pairs: t counts halves from `whole` on
     long long u, end;  // split: the unit's run of steps
     __device__ Tiles(const MxGemm& g_, const Routing& rt_, int KS_, int id, int units_, bool split)
         : g(g_), rt(rt_), NB((g_.N + TR - 1) / TR), KS(KS_), units(units_), t(id), u(-1), end(0) {
         total = NB * (grouped(g) ? rt.cum[g.E] : (g.R + g.plan.nt - 1) / g.plan.nt);
-        if (PAIR && g.plan.halves) total *= 2;
+        if constexpr (PAIR) {
+            whole = min(total, g.plan.halves);
+            total += total - whole;
+        }
         // Runs of whole tiles lose up to a tile's time in the last round; past eight rounds that is little.
         if (split && (2 * total <= units || (total > units && total < 8 * units && total % units))) {
             const int parts = 2 * total <= units ? 2 * total : units;
@@ -118,9 +121,9 @@ struct Tiles {
             u += o.k1 - o.k0;
         } else {
             if (t >= total) return false;
-            if (PAIR && g.plan.halves) {
-                tile = t >> 1;
-                if (t & 1) o.k0 = KS >> 1;
+            if (PAIR && t >= whole) {
+                tile = whole + ((t - whole) >> 1);
+                if ((t - whole) & 1) o.k0 = KS >> 1;
                 else o.k1 = KS >> 1;
             }
             t += units;

@@ -6,6 +6,7 @@
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
 #include <cuda_runtime.h>
+#include <limits.h>
 #include <stddef.h>
 #include <stdint.h>
 
@@ -251,11 +252,12 @@ constexpr int kMxRows = 256;   // operand rows of a token block at most,
 constexpr int kMxRows2 = 192;  // and with two accumulators to a CTA
 constexpr int kMxTopk = 64;    // pairs of a token at most
 // What the host decides for a product over R rows: the mode, the tokens of a block at most, scale blocks per 128
-// columns of a slot, and whether tiles may be cut along K between two CTAs, or are between two pairs of them, which then
-// add into outputs that the quantiser zeroed.
+// columns of a slot, and whether tiles may be cut along K between two CTAs, or some are between two pairs of them, which then
+// add into outputs that the quantiser zeroed: those from column `zero` on.
 struct MxPlan {
     int mode, nt, nblk, split;
-    int pair, halves;  // two CTAs to a tile (launch_mx_pair); tiles cut in half along K
+    int pair, halves;  // two CTAs to a tile (launch_mx_pair); the first tile that is cut in half along K
+    int zero;
 };
 MxPlan mx_plan(bool a16, int R, int N, int K, int E);
 inline long long mx_slots(int R, int E, int nt) { return E ? (long long)R / nt + E + 1 : ((long long)R + nt - 1) / nt; }
@@ -274,7 +276,7 @@ struct MxAct {
     uint8_t* codes;   // E2M1 [R][K / 2], digits [8 R][K / 2], or E4M3 parts [2][R][K]
     uint8_t* scales;  // [slots][K / 128][nblk][512]
     float* factors;   // digits: what each sorted row's sums are to be multiplied by
-    float* y;         // the rows' outputs, zeroed here if tiles are cut, and for pairs of no expert
+    float* y;         // the rows' outputs, zeroed here from plan.zero on, and for pairs of no expert
     int N;
     unsigned* err;
 };
