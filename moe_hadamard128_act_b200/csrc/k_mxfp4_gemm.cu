@@ -399,21 +399,24 @@ MxPlan mx_plan(bool a16, int R, int N, int K, int E) {
     MxPlan p;
     int halved = 0;
     const long long per = E ? ((long long)R + E - 1) / E : R;  // rows an expert
-    // Digits up to two blocks of one weight (21504 x 5376 at 32 rows 24.9 us against 26.5, at 48 rows 27.1 against
-    // 28.6, at 64 rows parts take 27.3), or 20 rows an expert (128 of 1408 x 2816 at 280 tokens 70.6 against 76.7, at
-    // 384 tokens 88.0 against 79.9).
-    p.mode = !a16 ? kMxA4 : per <= (E ? 20 : 48) ? kMxDigits : kMxParts;
+    // Digits for one block of one weight (21504 x 5376 at 24 rows 18.7 us; at 25 rows parts take 22.3 and digits 24.4),
+    // for more while there are two CTAs to a tile (2816 x 5376 at 72 rows 11.4 us against 13.1 as parts, at 96 rows 14.5
+    // against 13.5), and up to 20 rows an expert (128 of 1408 x 2816 at 280 tokens 70.6 us against 76.7, at 384 tokens
+    // 88.0 against 79.9).
+    const long long most = kMxRows2 / mx_planes(kMxDigits), digit_tiles = (N + TM - 1) / TM * ((per + most - 1) / most);
+    const bool digits = E ? per <= 20 : per <= most || (per <= 6 * most && 2 * digit_tiles <= kPlanSms);
+    p.mode = !a16 ? kMxA4 : digits ? kMxDigits : kMxParts;
     const int P = mx_planes(p.mode);
     if (p.mode == kMxDigits) {
         // Cut evenly, an even number of tokens; for experts 1.6 times the average count, so that most are one block (a
         // block costs its own rows alone, but a second one reads the weights again) and few ring slots go to rows
         // that are not there (128 experts of 1408 x 2816, 200 tokens: 63.2 us against 65.2 at twice the average).
-        const long long most = kMxRows2 / P, b = (R + most - 1) / most, nt = E ? (8 * per + 4) / 5 : (R + b - 1) / b;
+        const long long b = (R + most - 1) / most, nt = E ? (8 * per + 4) / 5 : (R + b - 1) / b;
         p.nt = (int)(((nt < most ? nt : most) + 1) / 2 * 2);
         p.pair = 0;
     } else if (E && per * P < kMxRows2) {
-        const long long most = kMxRows2 / P;
-        p.nt = (int)((2 * per < most ? 2 * per : most) + 15) / 16 * 16;
+        const long long wide = kMxRows2 / P;
+        p.nt = (int)((2 * per < wide ? 2 * per : wide) + 15) / 16 * 16;
         // Experts with 4-bit activations wait for their weights longer than for their rows: pairs of CTAs take 128 of
         // 1408 x 2816 at 400 tokens to 60.8 us from 58.9, at 2048 tokens to 91.5 from 94; parts gain everywhere (400
         // tokens 80 against 96).

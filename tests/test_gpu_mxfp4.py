@@ -508,3 +508,16 @@ def test_forward_last_tiles_cut_along_k(Q, fmt, M, N, K, had):
     close(y, *X.forward(x, W, fmt, bool(had)))
     for _ in range(5):
         assert torch.equal(Q.qlinear_forward(xd, c, s, None, fmt, N, flags=had), y)
+
+
+@pytest.mark.parametrize("M,N,K", [(25, 9473, 256), (64, 9400, 2048), (100, 19000, 2176), (300, 9000, 1152), (90, 2000, 640),
+                                   (144, 500, 384), (145, 500, 384)])
+def test_forward_16_bit_either_side_of_digits(Q, M, N, K):
+    # few rows of a large weight and many of a small one: as parts, some tiles halved, or as digits of several blocks
+    x = x_bits(M, K, seed=8)
+    c, s, W = weight(Q, N, K, seed=8)
+    xd = dev_bf16(x)
+    y = torch.full((M, N), float("nan"), device="cuda")
+    Q.qlinear_forward(xd, c, s, None, 16, N, y=y)
+    close(y, *X.forward(x, W, 16))
+    assert torch.equal(Q.qlinear_forward(xd, c, s, None, 16, N), y)
