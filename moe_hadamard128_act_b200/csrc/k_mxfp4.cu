@@ -6,8 +6,9 @@
 // 32-byte load of bf16): the rotation's shuffles stay inside the eight, a
 // 32-block is 2 lanes, and the 128 columns' four scale bytes are one word of
 // the scale layout (mx_layout.cuh).  With half as many values a lane the work
-// around the values, not the memory, set the time.  Bound by HBM: 2 (bf16) or 4 (fp32) bytes in
-// and 17/32 byte out per value.
+// around the values, not the memory, set the time (16384 x 5376 and back 82 us
+// against 77).  Bound by HBM: 2 (bf16) or 4 (fp32) bytes in and 17/32 byte out
+// per value; with the way back 5.8 TB/s.
 #include "mx_layout.cuh"
 #include "ql_internal.h"
 
@@ -265,8 +266,7 @@ __global__ void __launch_bounds__(kActWarps * 32) k_mx_act(const MxAct a) {
 // its counts, chunks and tiles.  A CTA an expert, and one more for the pairs of no expert, which flags them and
 // fills the tail of perm with -1.  Every CTA reads all ids, each warp a run of them 128 at a time:
 // first it counts its expert's pairs and those of the experts before, then, knowing the other warps' counts, it
-// writes.  Bound by latency: 16384 pairs of 128 experts
-// take 6 us less than moe_permute's histogram.
+// writes.  Bound by latency: 16384 pairs of 128 experts take 6 us less than moe_permute's histogram.
 constexpr int kRouteWarps = 16;
 __global__ void __launch_bounds__(kRouteWarps * 32) k_mx_route(const int32_t* ids, int P, int E, int32_t* offsets,
                                                                int32_t* perm, int32_t* inv, unsigned* err) {

@@ -38,8 +38,8 @@
 //
 // Warp roles: warp 0 brings in the weights, which wait for nothing, warp 2 the
 // activations, once the quantiser before this kernel is done (programmatic
-// dependent launch); warp 1 issues the scale copies and MMAs; warps 4..7 store the sums, 32 consecutive outputs of a token
-// per warp and instruction.
+// dependent launch); warp 1 issues the scale copies and MMAs; warps 4..11 store
+// the sums, 32 consecutive outputs of a token per warp and instruction.
 //
 // All waits are bounded; on a timeout the CTA sets QL_DEVERR_TIMEOUT and winds
 // down without leaving tensor memory allocated, MMAs running or copies in

@@ -1,7 +1,7 @@
 // ql_tmap.cu -- host-side construction of TMA tensor maps for 2-D matrices of
 // bytes (packed weights, int8 activations), of 4-bit codes that the copy
-// spreads to bytes or of scale blocks, cached by (address, shape, box, swizzle, element) since the
-// same weight is encoded again on every call.
+// spreads to bytes or of scale blocks, cached by (address, shape, box, swizzle,
+// element) since the same weight is encoded again on every call.
 #include <mutex>
 
 #include <cudaTypedefs.h>
