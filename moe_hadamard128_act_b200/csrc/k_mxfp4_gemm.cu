@@ -167,7 +167,7 @@ __global__ void __launch_bounds__(kThreads, 1) k_mx_gemm(const __grid_constant__
                 if (step >= ahead) {
                     // The first steps' weights are enough until the activations are there, whose copies would
                     // queue behind any more.
-                    if (step == ahead) asm volatile("griddepcontrol.wait;\n" ::: "memory");
+                    if (step == (grouped(g) ? kFirst : ahead)) asm volatile("griddepcontrol.wait;\n" ::: "memory");
                     if (!__all_sync(kFull, mbar_wait(bar(B_EMPTY + s), ph, lim))) {
                         dead = true;
                         break;

@@ -167,10 +167,11 @@ __device__ __forceinline__ void route(const MxGemm& g, Routing& rt, int warp, in
             rt.ids[threadIdx.x] = e >= 0 && e < g.E ? e : g.E;
         }
         __syncthreads();
+        const int n = (g.R + 7) & ~7;
         for (int e = threadIdx.x; e <= g.E; e += kThreads) {
             int below = 0, size = 0;
 #pragma unroll 8
-            for (int i = 0; i < kMxFusedPairs; ++i) {
+            for (int i = 0; i < n; ++i) {
                 below += rt.ids[i] < e;
                 size += rt.ids[i] == e;
             }
@@ -181,7 +182,7 @@ __device__ __forceinline__ void route(const MxGemm& g, Routing& rt, int warp, in
             const int p = threadIdx.x, e = rt.ids[p];
             int r = 0;
 #pragma unroll 8
-            for (int i = 0; i < kMxFusedPairs; ++i) r += rt.ids[i] < e || (rt.ids[i] == e && i < p);
+            for (int i = 0; i < n; ++i) r += rt.ids[i] < e || (rt.ids[i] == e && i < p);
             if (e < g.E) rt.perm[r] = p;
         }
     } else {
@@ -193,26 +194,26 @@ __device__ __forceinline__ void route(const MxGemm& g, Routing& rt, int warp, in
     }
     __syncthreads();
     if (warp != 3) return;
-    // Sound segments make no more blocks than this.  Overlapping ones (offsets out of order) could make more tiles
-    // than a count holds: then there are none.
-    const int most = g.R / g.plan.nt + g.E;
-    int sum = 0;
-    for (int e0 = 0; e0 < g.E && sum <= most; e0 += 32) {
-        const int v = e0 + lane < g.E ? cum[e0 + lane] : 0;
-        int incl = v;
+    // A lane adds up a run of experts.  Sound segments make no more than `most` blocks.  Overlapping ones (offsets out
+    // of order) could make more tiles than a count holds: then there are none.
+    const int most = g.R / g.plan.nt + g.E, run = (g.E + 31) >> 5, e0 = min(lane * run, g.E), e1 = min(e0 + run, g.E);
+    long long own = 0;
+    for (int e = e0; e < e1; ++e) own += cum[e];
+    const int mine = (int)min(own, (long long)most + 1);
+    int incl = mine;
 #pragma unroll
-        for (int d = 1; d < 32; d <<= 1) {
-            const int up = __shfl_up_sync(kFull, incl, d);
-            if (lane >= d) incl += up;
-        }
-        if (e0 + lane < g.E) cum[e0 + lane] = sum + incl - v;
-        sum += __shfl_sync(kFull, incl, 31);
+    for (int d = 1; d < 32; d <<= 1) {
+        const int up = __shfl_up_sync(kFull, incl, d);
+        if (lane >= d) incl = min(incl + up, most + 1);
     }
-    if (sum > most) {
-        for (int e = lane; e < g.E; e += 32) cum[e] = 0;
-        sum = 0;
+    const int sum = __shfl_sync(kFull, incl, 31);
+    int at = sum > most ? 0 : incl - mine;
+    for (int e = e0; e < e1; ++e) {
+        const int v = sum > most ? 0 : cum[e];
+        cum[e] = at;
+        at += v;
     }
-    if (lane == 0) cum[g.E] = sum;
+    if (lane == 0) cum[g.E] = sum > most ? 0 : sum;
 }
 
 // The epilogue of one tile in two halves, for warp kEpiWarp0 + w: lanes 32 (w % 4) .. + 31 of the accumulator are
