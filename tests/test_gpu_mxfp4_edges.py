@@ -1,0 +1,86 @@
+"""MXFP4 on the GPU at the ends of its ranges: what 16-bit activations keep of every value, up to the largest
+bf16, and calls that the operators' other tests do not make."""
+import numpy as np
+import pytest
+import torch
+
+from oracle import mxfp4 as X
+from tests.gpu_util import dev, dev_bf16
+from tests.test_gpu_mxfp4 import FMTS, close, weight, x_bits
+
+pytestmark = pytest.mark.gpu
+
+
+@pytest.fixture(scope="module")
+def Q():
+    from moe_hadamard128_act_b200 import build as qbuild
+    qbuild.build()
+    from moe_hadamard128_act_b200 import qlinear
+    qlinear.lib()
+    yield qlinear
+    assert qlinear.ql_get_device_error() == (0, 0)
+
+
+# ---- one value of x an output ----------------------------------------------------------------------------
+def one_hot(Q, N, K, byte=126):
+    """A packed weight with one code 1.0 a row, under scales 2^(byte - 127), and the column it is in."""
+    at = np.arange(N) * 37 % K
+    n = np.zeros((N, K), np.uint8)
+    n[np.arange(N), at] = 2
+    c, s, _ = Q.qlinear_pack(16, N, K, codes=dev(n), scales=dev(np.full((N, K // 32), byte, np.uint8)))
+    return c, s, at
+
+
+def spread_rows(M, K, seed, tops):
+    """bf16 bits: each block of 32 holds one value of a magnitude in [2^t, 2^(t + 1)), t one of `tops`, and others
+    1 to 24 powers of two below that, all with mantissas and signs of their own."""
+    rng = np.random.default_rng(seed)
+    t = np.repeat(rng.choice(tops, (M, K // 32)), 32, axis=1)
+    below = rng.integers(1, 25, (M, K))
+    first = rng.integers(0, 32, (M, K // 32)) + 32 * np.arange(K // 32)
+    np.put_along_axis(below, first, 0, axis=1)
+    field = t - below + 127
+    assert field.min() > 0 and field.max() < 255
+    return (rng.integers(0, 2, (M, K)) << 15 | field << 7 | rng.integers(0, 128, (M, K))).astype(np.uint16)
+
+
+def kept(got, x, fmt, at, scale=0.5):
+    """Each output is one value of x~: 16-bit activations exact from 2^-14 of the largest magnitude of the value's
+    32 up and within 2^-22 of that largest below, 4-bit ones what their codes stand for."""
+    v = X.activations(x, fmt, False)
+    got = got.cpu().numpy().astype(np.float64) / scale
+    if fmt == X.MXFP4A4_G32:
+        assert np.array_equal(got, v[:, at])
+        return
+    top = np.repeat(np.abs(v).reshape(len(v), -1, 32).max(-1), 32, axis=1)
+    off, exact = np.abs(got - v[:, at]), (np.abs(v) >= top * 2.0 ** -14)[:, at]
+    assert exact.any() and not exact.all()
+    assert not off[exact].any()
+    assert (off <= 2.0 ** -22 * top[:, at]).all()
+
+
+# rows as digits: tiles cut along K, one block, whole tiles, several blocks; as parts: pairs of CTAs, with halved tiles
+SHAPES = [(1, 512, 512), (3, 640, 256), (24, 512, 384), (8, 9600, 384), (100, 512, 384), (150, 512, 384), (200, 512, 512),
+          (40, 9600, 256), (64, 9400, 2048)]
+
+
+@pytest.mark.parametrize("fmt", FMTS)
+@pytest.mark.parametrize("M,N,K", SHAPES)
+def test_every_value_of_x_is_kept_up_to_the_largest(Q, fmt, M, N, K):
+    c, s, at = one_hot(Q, N, K)
+    x = spread_rows(M, K, M, [0, 126, 127])
+    x[0, 5] = 0xFF7F  # the lowest bf16, as masks use it
+    kept(Q.qlinear_forward(dev_bf16(x), c, s, None, fmt, N), x, fmt, at)
+
+
+@pytest.mark.parametrize("fmt", FMTS)
+@pytest.mark.parametrize("counts", [[1, 0, 5, 2], [60, 0, 30, 6], [200, 1, 40, 3]])  # digits (16-bit x), parts, parts
+def test_every_value_of_x_is_kept_by_experts(Q, fmt, counts):
+    N, K, E = 300, 384, len(counts)
+    c, s, at = one_hot(Q, N, K)
+    offsets = np.concatenate([[0], np.cumsum(counts)]).astype(np.int32)
+    R = int(offsets[-1])
+    x = spread_rows(R, K, R, [0, -60, 70, 127])
+    kept(Q.qlinear_grouped(dev_bf16(x), dev(offsets), c.repeat(E), s.repeat(E), E, N, fmt), x, fmt, at)
+    ids = np.repeat(np.arange(E, dtype=np.int32), counts)[:, None]
+    kept(Q.moe_gate_up(dev_bf16(x), dev(ids), c.repeat(E), s.repeat(E), E, N, fmt=fmt, flags=0)[:, 0], x, fmt, at)
