@@ -309,8 +309,9 @@ int qlinear_grouped_workspace_size(const ql_experts* experts, int R, size_t* byt
  * moe_permute makes them; y fp32 [R, N].  Rows outside every segment (before
  * offsets[0], from offsets[E] on) are neither read nor written.  An expert whose
  * two offsets are out of order or out of [0, R] is skipped and sets
- * QL_DEVERR_BOUNDS; what rows hold that other experts' segments then share is
- * undefined.  E <= 1024; `experts` is a host pointer; codes 32-byte aligned. */
+ * QL_DEVERR_BOUNDS; the other experts' rows are as ever, except that what
+ * segments hold that then overlap, or are not in ascending order, is undefined.
+ * E <= 1024; `experts` is a host pointer; codes 32-byte aligned. */
 int qlinear_grouped(const void* x, const int32_t* offsets, const ql_experts* experts, int R, float* y, void* ws,
                     size_t ws_bytes, void* stream);
 

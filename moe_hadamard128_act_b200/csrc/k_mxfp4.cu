@@ -177,11 +177,7 @@ __global__ void __launch_bounds__(kActWarps * 32) k_mx_act(const MxAct a) {
         }
     } else if (threadIdx.x < 32) {
         int e = 0, first = 0, end = a.R;
-        if (a.offsets) {
-            e = mx_warp_search(a.E, x, [&](int i) { return __ldg(a.offsets + i); });
-            end = 0;
-            if (e >= 0) mx_segment(a.offsets, e, a.R, first, end);  // a row outside it is no expert's
-        }
+        if (a.offsets) e = mx_expert_of(a.offsets, a.E, a.R, x, first, end);
         if (threadIdx.x == 0) place(0, x, x, e, first, end);
     }
     __syncthreads();

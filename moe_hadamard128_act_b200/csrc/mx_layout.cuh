@@ -54,6 +54,23 @@ __device__ __forceinline__ int mx_warp_search(int E, int v, Key key) {
     return base + 31 - __clz(m | 1u);
 }
 
+// The expert whose segment row r lies in, and the segment, by a whole warp; -1: none.  Among offsets in order it is the
+// last that starts at or before r.  Beside offsets that are not, the search may miss it: then all experts are looked at.
+__device__ __forceinline__ int mx_expert_of(const int32_t* offsets, int E, int R, int r, int& a, int& b) {
+    const int e = mx_warp_search(E, r, [&](int i) { return __ldg(offsets + i); });
+    if (e >= 0 && mx_segment(offsets, e, R, a, b) && r >= a && r < b) return e;
+    int found = E;  // the lane's, of those that it looks at; the loads wait for nothing
+#pragma unroll 4
+    for (int i = threadIdx.x & 31; i < E; i += 32) {
+        const int first = __ldg(offsets + i), end = __ldg(offsets + i + 1);
+        if (first >= 0 && first <= r && r < end && end <= R) found = min(found, i);
+    }
+    found = __reduce_min_sync(kFull, found);
+    if (found < E && mx_segment(offsets, found, R, a, b)) return found;
+    a = b = 0;
+    return -1;
+}
+
 // Eight fp32 values to E2M1 by the hardware conversion (round to nearest even, saturating to +-6), the first in
 // the low nibble.
 __device__ __forceinline__ uint32_t cvt_e2m1x8(const float v[8]) {

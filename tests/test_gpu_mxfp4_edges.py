@@ -84,3 +84,36 @@ def test_every_value_of_x_is_kept_by_experts(Q, fmt, counts):
     kept(Q.qlinear_grouped(dev_bf16(x), dev(offsets), c.repeat(E), s.repeat(E), E, N, fmt), x, fmt, at)
     ids = np.repeat(np.arange(E, dtype=np.int32), counts)[:, None]
     kept(Q.moe_gate_up(dev_bf16(x), dev(ids), c.repeat(E), s.repeat(E), E, N, fmt=fmt, flags=0)[:, 0], x, fmt, at)
+
+
+# ---- segments of experts beside a bad one -------------------------------------------------------------------
+def bad_offsets():
+    yield [0, 10, 20, -1, 40], 40
+    yield [0, 10, -3, 30, 40], 40
+    yield [0, 10, 1 << 30, 20, 40], 40
+    for bad in (-5, 1 << 20, 0):  # among many experts, where the search for a row's expert takes strides
+        for e in (4, 48, 50, 99):
+            offsets = [3 * i for i in range(101)]
+            offsets[e] = bad
+            yield offsets, 300
+
+
+@pytest.mark.parametrize("fmt", FMTS)
+@pytest.mark.parametrize("offsets,R", list(bad_offsets()))
+def test_grouped_sound_segments_beside_bad_offsets(Q, fmt, offsets, R):
+    E, N, K = len(offsets) - 1, 130, 256
+    x = x_bits(R, K, seed=3)
+    c, s, W = weight(Q, N, K, seed=1)
+    y = torch.full((R, N), 7.0, device="cuda")
+    ws = torch.full((Q.qlinear_grouped_workspace_size(E, N, K, fmt, 0, R),), 0x7F, dtype=torch.uint8, device="cuda")
+    Q.qlinear_grouped(dev_bf16(x), dev(np.array(offsets, np.int32)), c.repeat(E), s.repeat(E), E, N, fmt, y=y, ws=ws)
+    assert Q.ql_get_device_error() == (6, Q.DEVERR_BOUNDS)
+    got = y.cpu().numpy().astype(np.float64)
+    claims = np.zeros(R, int)
+    for a, b in zip(offsets, offsets[1:]):
+        if 0 <= a <= b <= R:
+            claims[a:b] += 1
+    ref, bound = X.forward(x, W, fmt)
+    one = claims == 1
+    close(got[one], ref[one], bound[one])
+    assert (got[claims == 0] == 7.0).all()
