@@ -167,13 +167,42 @@ def _new(stream, device, dtype, *size) -> torch.Tensor:
         return torch.empty(*size, dtype=dtype, device=device)
 
 
+def _output(y, stream, device, *size):
+    """The fp32 output (the caller's, or a new one) and its address."""
+    if y is not None:
+        return y, _ptr(y)
+    y = _new(stream, device, torch.float32, *size)
+    return y, y.data_ptr()
+
+
+def _workspace(ws, need: int, stream, device):
+    """A workspace of at least `need` bytes (the caller's, if it is large enough), its address and its size."""
+    if ws is not None and ws.nbytes >= need:
+        return ws, _ptr(ws), ws.nbytes
+    need = max(need, 16)
+    ws = _new(stream, device, torch.uint8, need)
+    return ws, ws.data_ptr(), need
+
+
 def _is_mxfp4(fmt: int) -> bool:
     return fmt == MXFP4_G32 or fmt == MXFP4A4_G32
 
 
-def _mx_check(what: str, fmt: int, N: int, K: int, E: int, codes, scales, y, shape):
-    """The product's tensors have the sizes that its kernels take for granted."""
+def _same_device(what: str, first, *others):
+    device = first.get_device()
+    for t in others:
+        if t is not None and t.get_device() != device:
+            raise ValueError(f"{what}: every tensor must be on the same device")
+
+
+def _mx_check(what: str, fmt: int, N: int, K: int, E: int, x, codes, scales, rows, y, shape, ws):
+    """The product's tensors have the sizes and the device that its kernels take for granted."""
     cb, sb, _ = qlinear_packed_sizes(fmt, N, K)
+    device = x.get_device()
+    if codes.get_device() != device or scales.get_device() != device or (rows is not None and rows.get_device() != device):
+        _same_device(what, x, codes, scales, rows)
+    if y is not None or ws is not None:
+        _same_device(what, x, y, ws)
     if codes.nbytes != E * cb or scales.nbytes != E * sb:
         raise ValueError(f"{what}: {E} x [{N}, {K}] take {E * cb} code and {E * sb} scale bytes")
     if y is not None and (y.dtype != torch.float32 or y.shape != shape):
@@ -197,6 +226,8 @@ def qlinear_workspace_size(fmt: int, flags: int, M: int, N: int, K: int) -> int:
 
 
 def _experts_struct(E, N, K, fmt, flags, codes, scales):
+    if not (codes.is_contiguous() and scales.is_contiguous()):
+        raise ValueError("expected contiguous codes and scales")
     return ql_experts(E, N, K, fmt, flags, codes.data_ptr(), scales.data_ptr())
 
 
@@ -224,6 +255,8 @@ def qlinear_pack(fmt: int, N: int, K: int, W: torch.Tensor | None = None, codes:
             raise ValueError(f"W must be an fp32 tensor of shape ({N}, {K})")
         if codes is not None and (codes.nbytes != N * K or scales is None or scales.nbytes != N * K // 32):
             raise ValueError(f"[{N}, {K}] take {N * K} code numbers and {N * K // 32} scales, a byte each")
+        if codes is not None:
+            _same_device("qlinear_pack", codes, scales)
     c_out, s_out = (_new(stream, dev, torch.uint8, max(n, 16)) for n in (cb, sb))
     z_out = _new(stream, dev, torch.uint8, max(zb, 16)) if zb else None
     _on(dev, "qlinear_pack", _ptr(W), _ptr(codes), _ptr(scales), _ptr(zeros), fmt, flags, N, K, _ptr(c_out),
@@ -240,14 +273,12 @@ def qlinear_forward(x: torch.Tensor, codes: torch.Tensor, scales: torch.Tensor, 
         raise ValueError("x must be a 2-D bf16 tensor")
     M, K = x.shape
     if _is_mxfp4(fmt):
-        _mx_check("qlinear_forward", fmt, N, K, 1, codes, scales, y, (M, N))
-    if y is None:
-        y = _new(stream, x.device, torch.float32, M, N)
-    need = qlinear_workspace_size(fmt, flags, M, N, K)
-    if ws is None or ws.numel() < need:
-        ws = _new(stream, x.device, torch.uint8, max(need, 16))
-    _on(x.device, "qlinear_forward", _ptr(x), _ptr(codes), _ptr(scales), _ptr(zeros), fmt, flags, M, N, K, _ptr(y),
-        _ptr(ws), ws.numel(), stream=stream)
+        _mx_check("qlinear_forward", fmt, N, K, 1, x, codes, scales, None, y, (M, N), ws)
+    device = x.device
+    y, out = _output(y, stream, device, M, N)
+    ws, at, size = _workspace(ws, qlinear_workspace_size(fmt, flags, M, N, K), stream, device)
+    _on(device, "qlinear_forward", _ptr(x), _ptr(codes), _ptr(scales), _ptr(zeros), fmt, flags, M, N, K, out, at, size,
+        stream=stream)
     return y
 
 
@@ -345,6 +376,7 @@ def mxfp4_dequant(codes: torch.Tensor, scales: torch.Tensor, N: int, K: int, out
         out = _new(stream, codes.device, torch.bfloat16, N, K)
     elif out.dtype != torch.bfloat16 or tuple(out.shape) != (N, K):
         raise ValueError(f"out must be a bf16 tensor of shape ({N}, {K})")
+    _same_device("mxfp4_dequant", codes, scales, out)
     _on(codes.device, "mxfp4_dequant", _ptr(codes), _ptr(scales), N, K, _ptr(out), stream=stream)
     return out
 
@@ -373,20 +405,22 @@ def moe_gate_up(x: torch.Tensor, topk_ids: torch.Tensor, codes: torch.Tensor, sc
                 y: torch.Tensor | None = None, ws: torch.Tensor | None = None, stream=None) -> torch.Tensor:
     """y [T, topk, N] fp32 for stacked expert weights (codes [E*N*K], scales)."""
     T, K = x.shape
-    topk = topk_ids.shape[1]
+    pairs = topk_ids.shape
+    topk = pairs[1]
     if _is_mxfp4(fmt):
-        _rows(x, "moe_gate_up")
-        if topk_ids.dtype != torch.int32 or topk_ids.shape != (T, topk):
+        if x.dtype != torch.bfloat16:
+            raise ValueError("moe_gate_up: x must be a 2-D bf16 tensor")
+        if topk_ids.dtype != torch.int32 or pairs != (T, topk):
             raise ValueError(f"topk_ids must be an int32 tensor of shape ({T}, topk)")
-        _mx_check("moe_gate_up", fmt, N, K, E, codes, scales, y, (T, topk, N))
+        _mx_check("moe_gate_up", fmt, N, K, E, x, codes, scales, topk_ids, y, (T, topk, N), ws)
+    elif not (codes.is_cuda and scales.is_cuda):
+        raise ValueError("expected CUDA codes and scales")
     ex = _experts_struct(E, N, K, fmt, flags, codes, scales)
-    need = moe_workspace_size(E, N, K, fmt, flags, T, topk)
-    if ws is None or ws.numel() < need:
-        ws = _new(stream, x.device, torch.uint8, max(need, 16))
-    if y is None:
-        y = _new(stream, x.device, torch.float32, T, topk, N)
-    _on(x.device, "moe_gate_up", _ptr(x), _ptr(topk_ids), _ptr(topk_weights), ctypes.byref(ex), T, topk, _ptr(y),
-        _ptr(ws), ws.numel(), stream=stream)
+    device = x.device
+    ws, at, size = _workspace(ws, moe_workspace_size(E, N, K, fmt, flags, T, topk), stream, device)
+    y, out = _output(y, stream, device, T, topk, N)
+    _on(device, "moe_gate_up", _ptr(x), _ptr(topk_ids), _ptr(topk_weights), ctypes.byref(ex), T, topk, out, at, size,
+        stream=stream)
     return y
 
 
@@ -406,17 +440,14 @@ def qlinear_grouped(x: torch.Tensor, offsets: torch.Tensor, codes: torch.Tensor,
     offsets[e] .. offsets[e + 1] (int32 [E + 1] on the device).  Rows outside every segment are left as they
     were: uninitialised when y is allocated here."""
     R, K = _rows(x, "qlinear_grouped")
-    if offsets.dtype != torch.int32 or offsets.numel() != E + 1:
+    if offsets.dtype != torch.int32 or offsets.nbytes != 4 * (E + 1):
         raise ValueError(f"offsets must be an int32 tensor of {E + 1} elements")
-    _mx_check("qlinear_grouped", fmt, N, K, E, codes, scales, y, (R, N))
-    need = qlinear_grouped_workspace_size(E, N, K, fmt, flags, R)
-    if ws is None or ws.nbytes < need:
-        ws = _new(stream, x.device, torch.uint8, max(need, 16))
-    if y is None:
-        y = _new(stream, x.device, torch.float32, R, N)
+    _mx_check("qlinear_grouped", fmt, N, K, E, x, codes, scales, offsets, y, (R, N), ws)
     ex = _experts_struct(E, N, K, fmt, flags, codes, scales)
-    _on(x.device, "qlinear_grouped", _ptr(x), _ptr(offsets), ctypes.byref(ex), R, _ptr(y), _ptr(ws), ws.nbytes,
-        stream=stream)
+    device = x.device
+    ws, at, size = _workspace(ws, qlinear_grouped_workspace_size(E, N, K, fmt, flags, R), stream, device)
+    y, out = _output(y, stream, device, R, N)
+    _on(device, "qlinear_grouped", _ptr(x), _ptr(offsets), ctypes.byref(ex), R, out, at, size, stream=stream)
     return y
 
 

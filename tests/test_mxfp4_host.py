@@ -208,3 +208,47 @@ def test_binding_refuses_tensors_of_other_sizes(Q):
                      lambda: Q.qlinear_pack(fmt, 64, 128, codes=torch.zeros(64 * 128, dtype=torch.uint8), scales=sc)):
             with pytest.raises(ValueError, match="take|must be"):
                 call()
+
+
+def test_binding_refuses_stacked_weights_that_are_not_contiguous(Q):
+    import torch
+    E, N, K = 2, 128, 256
+    x, ids = torch.zeros(4, K, dtype=torch.bfloat16), torch.zeros(4, 2, dtype=torch.int32)
+    off = torch.zeros(E + 1, dtype=torch.int32)
+    c, sc = torch.zeros(E, N * K // 2, dtype=torch.uint8), torch.zeros(E, 1024, dtype=torch.uint8)
+    for fmt in (Q.MXFP4_G32, Q.MXFP4A4_G32):
+        for codes, scales in ((c.t(), sc), (c, sc.t()), (c.repeat(1, 2)[:, ::2], sc), (c, sc[:1].expand(E, -1))):
+            for call in (lambda: Q.qlinear_grouped(x, off, codes, scales, E, N, fmt),
+                         lambda: Q.moe_gate_up(x, ids, codes, scales, E, N, fmt=fmt)):
+                with pytest.raises(ValueError, match="contiguous"):
+                    call()
+
+
+def test_binding_refuses_tensors_of_two_devices(Q, monkeypatch):
+    import torch
+    E, N, K = 2, 128, 256
+
+    def on(device, *size, dtype=torch.uint8):
+        t = torch.zeros(*size, dtype=dtype)
+        places[id(t)] = device
+        kept.append(t)
+        return t
+
+    places, kept = {}, []
+    monkeypatch.setattr(torch.Tensor, "get_device", lambda t: places[id(t)])
+    x, ids = on(0, 4, K, dtype=torch.bfloat16), on(0, 4, 2, dtype=torch.int32)
+    off, y = on(0, E + 1, dtype=torch.int32), on(0, 4, N, dtype=torch.float32)
+    c, sc, ws = on(0, E, N * K // 2), on(0, E, 1024), on(0, 1 << 20)
+    c1, sc1, out = on(0, N * K // 2), on(0, 1024), on(0, N, K, dtype=torch.bfloat16)
+    n, b = on(0, N, K), on(0, N, K // 32)
+    for fmt in (Q.MXFP4_G32, Q.MXFP4A4_G32):
+        for call, tensors in ((lambda: Q.qlinear_grouped(x, off, c, sc, E, N, fmt, y=y, ws=ws), (off, c, sc, y, ws)),
+                              (lambda: Q.moe_gate_up(x, ids, c, sc, E, N, fmt=fmt, ws=ws), (ids, c, sc, ws)),
+                              (lambda: Q.qlinear_forward(x, c1, sc1, None, fmt, N, y=y, ws=ws), (c1, sc1, y, ws)),
+                              (lambda: Q.mxfp4_dequant(c1, sc1, N, K, out), (sc1, out)),
+                              (lambda: Q.qlinear_pack(fmt, N, K, codes=n, scales=b), (b,))):
+            for t in tensors:
+                places[id(t)] = 1
+                with pytest.raises(ValueError, match="the same device"):
+                    call()
+                places[id(t)] = 0
