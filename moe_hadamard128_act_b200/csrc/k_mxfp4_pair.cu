@@ -26,8 +26,9 @@
 // two pairs each (MxPlan::halves); as in k_mxfp4_gemm.cu both add into zeroed outputs, in either order.  The epilogue's two forms are
 // apart because one that decides for every output costs 128 experts at 2048 tokens 103 us instead of 88.
 //
-// Waits are bounded as in k_mxfp4_gemm.cu; a CTA that gave up stays until copies
-// that it started have landed, and both CTAs leave together.
+// Waits are bounded as in k_mxfp4_gemm.cu.  Both CTAs leave together, once the
+// commits of all steps have arrived at their barriers and, if one of them gave up,
+// the copies that either started have landed.
 #include "mx_gemm.cuh"
 
 namespace ql {
@@ -51,11 +52,16 @@ __device__ __forceinline__ uint32_t cluster_rank() {
     asm volatile("mov.u32 %0, %cluster_ctarank;\n" : "=r"(r));
     return r;
 }
-// The address, in the even CTA, of this CTA's shared-memory address.
-__device__ __forceinline__ uint32_t in_even(uint32_t addr) {
+// The address, in the even (0) or odd (1) CTA, of this CTA's shared-memory address.
+__device__ __forceinline__ uint32_t in_cta(uint32_t addr, int rank) {
     uint32_t r;
-    asm volatile("mapa.shared::cluster.u32 %0, %1, 0;\n" : "=r"(r) : "r"(addr));
+    asm volatile("mapa.shared::cluster.u32 %0, %1, %2;\n" : "=r"(r) : "r"(addr), "r"(rank));
     return r;
+}
+__device__ __forceinline__ uint32_t in_even(uint32_t addr) { return in_cta(addr, 0); }
+// *p = v in one of the CTAs.
+__device__ __forceinline__ void put(const int* p, int rank, int v) {
+    asm volatile("st.shared::cluster.u32 [%0], %1;\n" ::"r"(in_cta(smem_u32(p), rank)), "r"(v) : "memory");
 }
 __device__ __forceinline__ void cluster_sync() {
     asm volatile("barrier.cluster.arrive.release.aligned;\nbarrier.cluster.wait.acquire.aligned;\n" ::: "memory");
@@ -120,12 +126,22 @@ __device__ __forceinline__ void pair_arrive(uint32_t cluster_bar) {
     asm volatile("mbarrier.arrive.release.cluster.shared::cluster.b64 _, [%0];\n" ::"r"(cluster_bar) : "memory");
 }
 
+// Wait until the barriers at `bar` of the ring's last steps before `steps` have completed those steps' phases.
+__device__ __forceinline__ bool pair_wait_last(uint32_t bar, int steps, int stages, unsigned long long lim = kWaitNs) {
+    for (int j = max(steps - stages, 0); j < steps; ++j)
+        if (!__all_sync(kFull, mbar_wait(bar + 8 * (j % stages), (j / stages) & 1, lim))) return false;
+    return true;
+}
+
 template <int MODE, int ROWS>  // ROWS: operand rows of a block at most
 __global__ void __launch_bounds__(kThreads, 1) k_mx_pair(const __grid_constant__ PairParams p) {
     extern __shared__ uint8_t smem_raw[];
     __shared__ __align__(8) uint64_t bars[NBARS];
     __shared__ uint32_t tmem_slot;
     __shared__ Routing rt;
+    __shared__ int gave_up;    // a wait of either CTA ran out (both CTAs' copies of it are set)
+    __shared__ int brought[4];  // even CTA: the steps that each CTA's two producers started
+    __shared__ int fed[2];      // the steps and tiles whose MMAs were committed
     constexpr bool PARTS = MODE == kMxParts;
     constexpr int KBS = PARTS ? 1 : 2;  // 128-column blocks per step
     const MxGemm& g = p.g;
@@ -143,6 +159,7 @@ __global__ void __launch_bounds__(kThreads, 1) k_mx_pair(const __grid_constant__
     const unsigned long long lim = wait_limit(g.err);
     bool dead = false;
     Tile ti;
+    if (threadIdx.x == 0) gave_up = 0;
     if (warp == 0 && elect()) {
         for (int s = 0; s < p.stages; ++s) {
             mbar_init(bar(B_FULL + s), 2);   // even CTA: its two producers' expect_tx, for both CTAs' copies
@@ -171,14 +188,14 @@ __global__ void __launch_bounds__(kThreads, 1) k_mx_pair(const __grid_constant__
 
     if (warp == 0) {  // ---- weights and their scales ----
         const bool leader = elect();
-        int s = 0, ph = 1;
+        int s = 0, ph = 1, step = 0;
         while (!dead && tiles.next(ti)) {
             const int e = uniform(ti.expert), wb = 2 * uniform(ti.wb) + rank;  // this CTA's 128 rows
             const int row = e * g.N + wb * TM;
             // Past the last row of all (an odd number of 128-row blocks) the scales are some block's: no output
             // comes of those rows.
             const int sf = (e * NB + min(wb, NB - 1)) * G;
-            for (int k = uniform(ti.k0), k1 = uniform(ti.k1); k < k1; ++k) {
+            for (int k = uniform(ti.k0), k1 = uniform(ti.k1); k < k1; ++k, ++step) {
                 if (!__all_sync(kFull, mbar_wait(bar(B_EMPTY + s), ph, lim))) {
                     dead = true;
                     break;
@@ -194,16 +211,19 @@ __global__ void __launch_bounds__(kThreads, 1) k_mx_pair(const __grid_constant__
                 if (++s == p.stages) { s = 0; ph ^= 1; }
             }
         }
+        if (leader) put(&brought[2 * rank], 0, step);
+        // The last steps' commits, which the other CTA's thread makes, arrive here before this CTA may leave.
+        if (!dead && !pair_wait_last(bar(B_EMPTY), step, p.stages, lim)) dead = true;
     } else if (warp == 2) {  // ---- activations and their scales ----
         const bool leader = elect();
         asm volatile("griddepcontrol.wait;\n" ::: "memory");  // the quantiser's codes and scales
-        int s = 0, ph = 1;
+        int s = 0, ph = 1, step = 0;
         while (!dead && tiles.next(ti)) {
             // the pair's columns: with 4-bit activations a multiple of 32, so that each half is whole 16-row boxes
             const int half = uniform(PARTS ? mx_pad16(ti.rows) : ((ti.rows + 31) & ~31) / 2);
             const int row = PARTS ? rank * g.R + uniform(ti.row0) : uniform(ti.row0) + rank * half;
             const int sf = uniform(ti.slot) * G * nblk;
-            for (int k = uniform(ti.k0), k1 = uniform(ti.k1); k < k1; ++k) {
+            for (int k = uniform(ti.k0), k1 = uniform(ti.k1); k < k1; ++k, ++step) {
                 if (!__all_sync(kFull, mbar_wait(bar(B_EMPTY + s), ph, lim))) {
                     dead = true;
                     break;
@@ -221,6 +241,7 @@ __global__ void __launch_bounds__(kThreads, 1) k_mx_pair(const __grid_constant__
                 if (++s == p.stages) { s = 0; ph ^= 1; }
             }
         }
+        if (leader) put(&brought[2 * rank + 1], 0, step);
     } else if (warp == 3 && rank == 0) {  // ---- scales to tensor memory ----
         const bool leader = elect();
         int s = 0, ph = 0, q = 0;  // q: the step's scale columns
@@ -263,7 +284,7 @@ __global__ void __launch_bounds__(kThreads, 1) k_mx_pair(const __grid_constant__
         if (leader) pair_commit_here(bar(B_DRAIN));
     } else if (warp == 1 && rank == 0) {  // ---- MMAs ----
         const bool leader = elect();
-        int s = 0, q = 0, qph = 0, tl = 0;
+        int s = 0, q = 0, qph = 0, tl = 0, step = 0;
         while (!dead && tiles.next(ti)) {
             const int b = p.nacc == 2 ? tl & 1 : 0, use = p.nacc == 2 ? tl >> 1 : tl;
             if (!__all_sync(kFull, pair_wait(bar(B_ACCE + b), (use & 1) ^ 1, lim))) {  // both epilogues are done
@@ -273,7 +294,7 @@ __global__ void __launch_bounds__(kThreads, 1) k_mx_pair(const __grid_constant__
             const int cols = uniform(PARTS ? 2 * mx_pad16(ti.rows) : (ti.rows + 31) & ~31);
             const uint32_t d = tmem + b * p.acc_cols, id0 = idesc<MODE>(PM, cols);
             const int k0 = uniform(ti.k0), k1 = uniform(ti.k1);
-            for (int k = k0; k < k1; ++k) {
+            for (int k = k0; k < k1; ++k, ++step) {
                 // the scales are in place, and with them the operands, which their copier waited for
                 if (!__all_sync(kFull, mbar_wait(bar(B_SF + q), qph, lim))) {
                     dead = true;
@@ -304,7 +325,13 @@ __global__ void __launch_bounds__(kThreads, 1) k_mx_pair(const __grid_constant__
             ++tl;
         }
         // Every copy and MMA issued must finish before tensor memory is freed.
-        if (leader) pair_commit_here(bar(B_DRAIN));
+        if (leader) {
+            pair_commit_here(bar(B_DRAIN));
+            for (int r = 0; r < 2; ++r) {
+                put(&fed[0], r, step);
+                put(&fed[1], r, tl);
+            }
+        }
         __syncwarp();
         mbar_wait(bar(B_DRAIN), 0);
     } else if (warp >= kEpiWarp0) {  // ---- epilogue ----
@@ -330,18 +357,29 @@ __global__ void __launch_bounds__(kThreads, 1) k_mx_pair(const __grid_constant__
             ++tl;
         }
     }
-    // All copies were consumed unless a wait ran out; then they are given time to land before the CTA's shared
-    // memory is released.
     if (dead) {
         atomicOr(g.err, (unsigned)QL_DEVERR_TIMEOUT);
-        const unsigned long long t0 = global_ns();
-        while (global_ns() - t0 < 2000000ull) {
+        if (lane == 0) {
+            put(&gave_up, 0, 1);
+            put(&gave_up, 1, 1);
         }
     }
     __syncwarp();
     fence_before();
     __syncthreads();
     cluster_sync();
+    // All copies were consumed unless a wait ran out.  Then those in flight, and commits, have to arrive before the CTAs'
+    // shared memory is released.  A step that not all four producers started ends this at the wait's bound.
+    if (*const_cast<volatile int*>(&gave_up)) {
+        if (warp == 0) {
+            pair_wait_last(bar(B_EMPTY), fed[0], p.stages);
+            pair_wait_last(bar(B_ACCF), fed[1], p.nacc);
+            if (rank == 0)
+                pair_wait_last(bar(B_FULL), max(max(brought[0], brought[1]), max(brought[2], brought[3])), p.stages);
+        }
+        __syncthreads();
+        cluster_sync();
+    }
     if (warp == 2) {
         fence_after();
         asm volatile("tcgen05.dealloc.cta_group::2.sync.aligned.b32 %0, %1;\n" ::"r"(tmem), "r"(kTmemCols));

@@ -117,3 +117,28 @@ def test_grouped_sound_segments_beside_bad_offsets(Q, fmt, offsets, R):
     one = claims == 1
     close(got[one], ref[one], bound[one])
     assert (got[claims == 0] == 7.0).all()
+
+
+# ---- waits that run out -------------------------------------------------------------------------------------
+@pytest.mark.parametrize("fmt", FMTS)
+@pytest.mark.parametrize("limit", [1, 1500, 6000])
+def test_pairs_that_gave_up_leave_nothing_behind(Q, fmt, limit):
+    # pairs of CTAs give up at once or some way into the product (or, with the longest bound, perhaps not at all); the
+    # calls that follow on the same SMs are right
+    M, N, K = 200, 5000, 2176
+    x = x_bits(M, K, seed=9)
+    c, s, W = weight(Q, N, K)
+    xd, ref = dev_bf16(x), X.forward(x, W, fmt)
+    few = X.forward(x[:3], W, fmt)
+    close(Q.qlinear_forward(xd, c, s, None, fmt, N), *ref)
+    for _ in range(3):
+        Q.ql_set_wait_limit(limit)
+        try:
+            Q.qlinear_forward(xd, c, s, None, fmt, N)
+        finally:
+            Q.ql_set_wait_limit(0)
+        y = [Q.qlinear_forward(xd, c, s, None, fmt, N), Q.qlinear_forward(xd[:3], c, s, None, fmt, N)]
+        status = Q.ql_get_device_error()
+        assert status in ((6, Q.DEVERR_TIMEOUT), (0, 0)) and (limit > 1 or status[0] == 6)
+        close(y[0], *ref)
+        close(y[1], *few)
