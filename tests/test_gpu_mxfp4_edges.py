@@ -66,6 +66,14 @@ SHAPES = [(1, 512, 512), (3, 640, 256), (24, 512, 384), (8, 9600, 384), (100, 51
 
 @pytest.mark.parametrize("fmt", FMTS)
 @pytest.mark.parametrize("M,N,K", SHAPES)
+def test_every_value_of_x_is_kept(Q, fmt, M, N, K):
+    c, s, at = one_hot(Q, N, K)
+    x = spread_rows(M, K, M, [0, 3, -40, 90, -90, 126])
+    kept(Q.qlinear_forward(dev_bf16(x), c, s, None, fmt, N), x, fmt, at)
+
+
+@pytest.mark.parametrize("fmt", FMTS)
+@pytest.mark.parametrize("M,N,K", SHAPES)
 def test_every_value_of_x_is_kept_up_to_the_largest(Q, fmt, M, N, K):
     c, s, at = one_hot(Q, N, K)
     x = spread_rows(M, K, M, [0, 126, 127])
