@@ -180,8 +180,8 @@ int qlinear_workspace_size(int fmt, int flags, int M, int N, int K, size_t* byte
  *      cores as eight 4-bit digits (few rows) or two 8-bit parts, each with a
  *      power-of-two scale per 32 values; their sum is exact for every value at
  *      least 2^-14 of the largest of its 32 and within 2^-22 of that largest
- *      otherwise.  (Digits of a block below 2^-105 in a row that reaches 2^-64
- *      end at 2^-129.)
+ *      otherwise.  (As digits, a block below 2^-105 in a row that reaches 2^-64
+ *      is held in multiples of 2^-127.)
  *   W_packed, scales, zeros: the packed weight (zeros only for int5).
  *   ws, ws_bytes: caller's device workspace, at least qlinear_workspace_size.
  * y is overwritten.  The floating-point sums may be accumulated in any order;
@@ -195,8 +195,9 @@ int qlinear_workspace_size(int fmt, int flags, int M, int N, int K, size_t* byte
  * (QL_EUNSUPPORTED above, in every MXFP4 call); a row of x with
  * a value that is not finite gives a row of y that is NaN, and a weight block
  * with scale byte 255 a NaN column; a sum that leaves fp32's range on the way is
- * infinite or NaN, and results below 2^-126 may be flushed to zero; the sums are
- * bit-reproducible. */
+ * infinite or NaN (with 16-bit x, whose first digit or part can be above the
+ * value, from products that add up to 2^127 in magnitude), and results below
+ * 2^-126 may be flushed to zero; the sums are bit-reproducible. */
 enum { QL_A16_MAX_K = 32768, QL_MXFP4_MAX_ROWS = 1 << 30 };
 int qlinear_forward(const void* x, const void* W_packed, const void* scales, const uint8_t* zeros, int fmt,
                     int flags, int M, int N, int K, float* y, void* ws, size_t ws_bytes, void* stream);

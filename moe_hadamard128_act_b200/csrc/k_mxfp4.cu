@@ -105,8 +105,9 @@ struct Place {
 };
 
 // Digits: 32, and a factor of 2^-32 on the row's sums, if no magnitude of the row (rotated and rounded as the
-// quantiser sees it) reaches 2^-64, else 0; by a whole warp.  The digits' scales end at 2^-127, which cuts a
-// block below 2^-105; beside a value of 2^-64 that is at most 2^-65 of it, and without one the row is moved up.
+// quantiser sees it) reaches 2^-64, else 0; by a whole warp.  The digits' scales end at 2^-127, which rounds a
+// block below 2^-105 to multiples of that; beside a value of 2^-64 the loss is at most 2^-64 of it, and without one the
+// row is moved up.
 constexpr uint32_t kSmallRow = 63u << 23;  // 2^-64
 __device__ __noinline__ int row_up(const __nv_bfloat16* x, int G, int rotate) {
     const int lane = threadIdx.x & 7;

@@ -163,7 +163,7 @@ __device__ __forceinline__ uint2 mx_quant16(const float v[16], uint32_t& byte) {
 
 // A 32-block of bf16 values as eight E2M1 digits, v = 2^e sum_p d_p 8^-p: e puts the block's largest magnitude
 // into [1, 2), v / 2^e is rounded to a multiple of 8^-7, and that number's digits in base 8 from -4 to 3 are all
-// E2M1 values.  So v is off by at most 2^-22 of the largest magnitude, and not at all down to 2^-15 of it.
+// E2M1 values.  So v is off by at most 2^-22 of the largest magnitude, and not at all down to 2^-14 of it.
 // byte: the first digit's scale; digit p's is byte - 3 p, so it is held at 21 or more: a block below 2^-105
 // loses its last digits, unless its whole row is small and was scaled up by 2^up (see k_mx_act).
 // The digits are taken in integers: 4 in every digit makes them 0 .. 7, three bits each, which are spread to

@@ -94,6 +94,23 @@ def test_every_value_of_x_is_kept_by_experts(Q, fmt, counts):
     kept(Q.moe_gate_up(dev_bf16(x), dev(ids), c.repeat(E), s.repeat(E), E, N, fmt=fmt, flags=0)[:, 0], x, fmt, at)
 
 
+@pytest.mark.parametrize("M", [3, 200])
+def test_blocks_of_small_magnitude_in_a_row_that_reaches_2_to_minus_64(Q, M):
+    # As digits (3 rows) a block below 2^-105 beside a value of 2^-64 or more is held in multiples of 2^-127.  So it is as
+    # parts (200 rows): the block's largest, 255 * 2^-113, lies in [2^-106, 2^-105), so hi has the scale 2^(-106 - 7) and
+    # lo, E4M3 in steps of 2^-9 and 2^-5 below hi, steps of 2^-127.  The weight's scale keeps the outputs in fp32's
+    # normal range.
+    N = K = 256
+    c, s, at = one_hot(Q, N, K, 127 + 60)
+    x = np.zeros((M, K), np.uint16)
+    x[:, 0] = 63 << 7  # 2^-64
+    x[:, 32:38] = [1, 2, 0x40, 0x7F, 7 << 7 | 0x35, 0x8000 | 21 << 7 | 0x7F]  # 2^-133 .. -255 * 2^-113
+    v = X.bf16_values(x).astype(np.float64)
+    got = Q.qlinear_forward(dev_bf16(x), c, s, None, 16, N).cpu().numpy().astype(np.float64) * 2.0 ** -60
+    v[:, 32:64] = np.rint(v[:, 32:64] * 2.0 ** 127) * 2.0 ** -127
+    assert np.array_equal(got, v[:, at])
+
+
 # ---- segments of experts beside a bad one -------------------------------------------------------------------
 def bad_offsets():
     yield [0, 10, 20, -1, 40], 40
