@@ -173,16 +173,15 @@ __device__ __forceinline__ uint32_t mx_digits_byte(uint32_t ex, int up) {
     return ex == 255 ? 255u : (uint32_t)max((int)ex + up, 21);  // 255: an infinity or a NaN
 }
 __device__ __forceinline__ void mx_digits8(const float* v, uint32_t byte, int up, uint32_t d[8]) {
-    // 2^-e has the exponent field f (0, a subnormal, for blocks that reach 2^127); past 254 as a product of two powers
-    // (with up only).  Then 8^7 = 2^21.
-    const int f = 254 - ((int)byte - up);
-    const float i0 = __uint_as_float(f == 0 ? 0x00400000u : (uint32_t)min(f, 254) << 23);
-    const float i1 = __uint_as_float((uint32_t)(127 + 21 + max(f - 254, 0)) << 23);
+    // 2^-e has the exponent field f: 0, a subnormal, for blocks that reach 2^127, and up to 254, for those below 2^-126 of a
+    // row scaled up, so 8^7 = 2^21 is a factor of its own.
+    const uint32_t f = 254u + (uint32_t)up - byte;
+    const float inv = __uint_as_float(f == 0 ? 0x00400000u : f << 23);
     constexpr uint32_t kLow = 0x0A0C0D0Eu, kHigh = 0x05040200u;  // E2M1 of -4 .. -1 and 0 .. 3
     uint32_t lo[4], hi[4];  // values 2 j and 2 j + 1 in a byte; digits 7 .. 4 and 3 .. 0 from the low byte up
 #pragma unroll
     for (int i = 0; i < 8; ++i) {
-        uint32_t u = (uint32_t)(__float2int_rn(v[i] * i0 * i1) + 0x924924);
+        uint32_t u = (uint32_t)(__float2int_rn(v[i] * inv * 0x1p21f) + 0x924924);
         // Fields moved up by multiply-adds (u + 15 f is u with its field f shifted by 4), which the integer pipe,
         // the busiest one here, does not see.
         u += (u & 0xFFF000u) * 15u;
