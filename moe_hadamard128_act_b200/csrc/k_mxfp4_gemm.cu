@@ -10,19 +10,13 @@
 //   16-bit activations, few rows (kind::mxf4): a token enters as eight rows of
 //     E2M1 digits in base 8, each with scales of its own, whose products the
 //     epilogue adds up.  The weights stream as fast as with 4-bit activations.
-//   16-bit activations, many rows (kind::mxf8f6f4): the weights' codes are
-//     spread to bytes by the copy engine (16 codes to 16 bytes) on their way into
-//     shared memory, and x enters as two E4M3 parts with scales of their own,
-//     x = hi + lo, the low parts being further operand rows: column c of the
-//     accumulator is the high part's sum of token c, column n16 + c the low
-//     part's, and the epilogue adds them.  A quarter of the digits' tensor work
-//     at half its rate, but the spreading copy brings only half as many codes a
-//     second, which is what few rows wait for.
+//   16-bit activations, many rows: as two parts, on pairs of CTAs alone
+//     (k_mxfp4_pair.cu).
 //
 // A tile is 128 weight rows (the MMA's M, tensor-memory lanes) by one token
 // block (its N: the block's operand rows rounded up to 16), so a decode batch and
 // a prefill differ in N alone.  A step is 128 bytes of every operand
-// row: 256 columns of K, or 128.  A ring slot holds the step's weight codes
+// row, 256 columns of K.  A ring slot holds the step's weight codes
 // (16 KB), its activation codes and both scale blocks; as many slots as shared
 // and tensor memory allow keep the weights streaming.  Each slot has its own
 // tensor-memory columns for its scales: they are rewritten only when the slot
@@ -55,25 +49,18 @@ constexpr int B_FULL = 0, B_EMPTY = kMaxStages, B_ACCF = 2 * kMaxStages, B_ACCE 
 
 struct MxParams {
     CUtensorMap tmW;         // weight codes: [E * N rows], box [128 rows][128 bytes of shared memory]
-    CUtensorMap tmX, tmXb;   // activation codes: [R or 2 R rows], boxes of 16 and 64 rows x 128 bytes
+    CUtensorMap tmX, tmXb;   // activation codes: [R or 8 R rows], boxes of 16 and 64 rows x 128 bytes
     MxGemm g;
     int stages, stage_bytes;     // ring
     int acc_cols, sf0, sf_cols;  // tensor memory: accumulator stride, first scale column, scale columns per slot
 };
 
-template <int MODE>
 __device__ __forceinline__ void mma(uint32_t d, uint64_t ad, uint64_t bd, uint32_t id, uint32_t sfa, uint32_t sfb,
                                     uint32_t acc_in) {
-    if constexpr (MODE == kMxParts)
-        asm volatile(
-            "{\n .reg .pred p;\n setp.ne.b32 p, %6, 0;\n"
-            " tcgen05.mma.cta_group::1.kind::mxf8f6f4.block_scale.scale_vec::1X [%0], %1, %2, %3, [%4], [%5], p;\n}\n" ::"r"(d),
-            "l"(ad), "l"(bd), "r"(id), "r"(sfa), "r"(sfb), "r"(acc_in));
-    else
-        asm volatile(
-            "{\n .reg .pred p;\n setp.ne.b32 p, %6, 0;\n"
-            " tcgen05.mma.cta_group::1.kind::mxf4.block_scale.scale_vec::2X [%0], %1, %2, %3, [%4], [%5], p;\n}\n" ::"r"(d),
-            "l"(ad), "l"(bd), "r"(id), "r"(sfa), "r"(sfb), "r"(acc_in));
+    asm volatile(
+        "{\n .reg .pred p;\n setp.ne.b32 p, %6, 0;\n"
+        " tcgen05.mma.cta_group::1.kind::mxf4.block_scale.scale_vec::2X [%0], %1, %2, %3, [%4], [%5], p;\n}\n" ::"r"(d),
+        "l"(ad), "l"(bd), "r"(id), "r"(sfa), "r"(sfb), "r"(acc_in));
 }
 // 512 bytes of scales: 32 rows of 16 bytes to 4 columns, the same in all four lane quarters.
 __device__ __forceinline__ void copy_scales(uint32_t col, uint64_t desc) {
@@ -91,8 +78,7 @@ __global__ void __launch_bounds__(kThreads, 1) k_mx_gemm(const __grid_constant__
     __shared__ __align__(8) uint64_t bars[NBARS];
     __shared__ uint32_t tmem_slot;
     __shared__ Routing rt;
-    constexpr bool PARTS = MODE == kMxParts;
-    constexpr int KBS = PARTS ? 1 : 2;  // 128-column blocks per step
+    constexpr int KBS = 2;  // 128-column blocks per step
     const MxGemm& g = p.g;
     const uint32_t base = (smem_u32(smem_raw) + 1023u) & ~1023u;
     auto bar = [&](int i) { return smem_u32(&bars[i]); };
@@ -113,7 +99,7 @@ __global__ void __launch_bounds__(kThreads, 1) k_mx_gemm(const __grid_constant__
         const uint32_t slot = base + s * p.stage_bytes, fb = bar(B_FULL + s);
         const uint8_t* sf = g.scales + (((long long)t.expert * NB + t.wb) * G + k * KBS) * 512;
         if (leader) {
-            mbar_expect_tx(fb, (PARTS ? A_BYTES / 2 : A_BYTES) + sfb);  // spread copies count the packed bytes
+            mbar_expect_tx(fb, A_BYTES + sfb);
             tma_load_2d(slot, &p.tmW, k * 128, t.expert * g.N + t.wb * TM, fb);
             bulk_load(slot + sa_off, sf, sfb, fb);
         }
@@ -190,8 +176,7 @@ __global__ void __launch_bounds__(kThreads, 1) k_mx_gemm(const __grid_constant__
         asm volatile("griddepcontrol.wait;\n" ::: "memory");  // the quantiser's codes and scales
         int step = 0, s = 0, ph = 1;
         while (!dead && tiles.next(ti)) {
-            const int cols = uniform(columns<MODE>(ti.rows)), row0 = uniform(ti.row0);
-            const int n = PARTS ? cols / 2 : cols;  // rows to bring, of each part
+            const int cols = uniform(mx_pad16(mx_planes(MODE) * ti.rows)), row = mx_planes(MODE) * uniform(ti.row0);
             const uint8_t* sf = g.xs + (long long)uniform(ti.slot) * G * nblk * 512;
             for (int k = uniform(ti.k0), k1 = uniform(ti.k1); k < k1; ++k, ++step) {
                 if (!__all_sync(kFull, mbar_wait(bar(B_EMPTY + s), ph, lim))) {
@@ -202,14 +187,10 @@ __global__ void __launch_bounds__(kThreads, 1) k_mx_gemm(const __grid_constant__
                 const uint32_t slot = base + s * p.stage_bytes, fb = bar(B_FULL + s);
                 if (leader) {
                     mbar_expect_tx(fb, cols * 128 + sfb);
-#pragma unroll
-                    for (int pl = 0; pl < (PARTS ? 2 : 1); ++pl) {
-                        const int row = MODE == kMxDigits ? 8 * row0 : pl * g.R + row0;
-                        const uint32_t dst = slot + b_off + pl * n * 128;
-                        int r = 0;
-                        for (; r + BIG <= n; r += BIG) tma_load_2d(dst + r * 128, &p.tmXb, k * 128, row + r, fb);
-                        for (; r < n; r += SMALL) tma_load_2d(dst + r * 128, &p.tmX, k * 128, row + r, fb);
-                    }
+                    const uint32_t dst = slot + b_off;
+                    int r = 0;
+                    for (; r + BIG <= cols; r += BIG) tma_load_2d(dst + r * 128, &p.tmXb, k * 128, row + r, fb);
+                    for (; r < cols; r += SMALL) tma_load_2d(dst + r * 128, &p.tmX, k * 128, row + r, fb);
                     bulk_load(slot + sb_off, sf + (long long)k * KBS * nblk * 512, sfb, fb);
                 }
                 if (++s == p.stages) { s = 0; ph ^= 1; }
@@ -226,7 +207,7 @@ __global__ void __launch_bounds__(kThreads, 1) k_mx_gemm(const __grid_constant__
                 dead = true;
                 break;
             }
-            const uint32_t d = tmem + b * p.acc_cols, id0 = idesc<MODE>(TM, uniform(columns<MODE>(ti.rows)));
+            const uint32_t d = tmem + b * p.acc_cols, id0 = idesc<MODE>(TM, uniform(mx_pad16(mx_planes(MODE) * ti.rows)));
             const int k0 = uniform(ti.k0), k1 = uniform(ti.k1);
             for (int k = k0; k < k1; ++k) {
                 if (!__all_sync(kFull, mbar_wait(bar(B_FULL + s), ph, lim))) {
@@ -250,10 +231,10 @@ __global__ void __launch_bounds__(kThreads, 1) k_mx_gemm(const __grid_constant__
                     }
 #pragma unroll
                     for (int j = 0; j < 4; ++j) {  // 32 bytes of every row: +2 in the descriptors' address field
-                        const int q = PARTS ? 0 : j >> 1, byte = PARTS ? j : 2 * (j & 1);  // its scales' block and byte
+                        const int q = j >> 1, byte = 2 * (j & 1);  // its scales' block and byte
                         if (q < kbs)
-                            mma<MODE>(d, ad + 2 * j, bd + 2 * j, id0 | (uint32_t)byte << 4 | (uint32_t)byte << 29,
-                                     sf + 4 * q, sfb + 4 * nblk * q, (k > k0 || j) ? 1u : 0u);
+                            mma(d, ad + 2 * j, bd + 2 * j, id0 | (uint32_t)byte << 4 | (uint32_t)byte << 29, sf + 4 * q,
+                                sfb + 4 * nblk * q, (k > k0 || j) ? 1u : 0u);
                     }
                     commit(bar(B_EMPTY + s));  // the slot and its scale columns may be refilled once these are done
                 }
@@ -303,8 +284,7 @@ cudaError_t run(const MxGemm& g, cudaStream_t s) {
     DeviceInfo di;
     cudaError_t e = device_info(&di);
     if (e != cudaSuccess) return e;
-    constexpr bool PARTS = MODE == kMxParts;
-    constexpr int P = mx_planes(MODE), KBS = PARTS ? 1 : 2;
+    constexpr int P = mx_planes(MODE), KBS = 2;
     MxParams p;
     p.g = g;
     const int nblk = g.plan.nblk, rows = P * g.plan.nt;  // operand rows of a full token block
@@ -319,9 +299,8 @@ cudaError_t run(const MxGemm& g, cudaStream_t s) {
     if (p.stages > kMaxStages) p.stages = kMaxStages;
     if (p.stages < 2) return cudaErrorInvalidValue;
     const int smem = p.stages * p.stage_bytes + 1024;
-    const long long wrows = (long long)g.E * g.N, xrows = (long long)P * g.R, xbytes = PARTS ? g.K : g.K / 2;
-    e = PARTS ? make_tmap_u4_spread(g.codes, wrows, g.K, TM, &p.tmW)
-              : make_tmap_2d(g.codes, wrows, g.K / 2, g.K / 2, 128, TM, CU_TENSOR_MAP_SWIZZLE_128B, &p.tmW);
+    const long long wrows = (long long)g.E * g.N, xrows = (long long)P * g.R, xbytes = g.K / 2;
+    e = make_tmap_2d(g.codes, wrows, xbytes, xbytes, 128, TM, CU_TENSOR_MAP_SWIZZLE_128B, &p.tmW);
     if (e == cudaSuccess) e = make_tmap_2d(g.xq, xrows, xbytes, xbytes, 128, SMALL, CU_TENSOR_MAP_SWIZZLE_128B, &p.tmX);
     p.tmXb = p.tmX;
     if (e == cudaSuccess && rows >= BIG)
@@ -420,12 +399,13 @@ MxPlan mx_plan(bool a16, int R, int N, int K, int E) {
         // Experts with 4-bit activations wait for their weights longer than for their rows: pairs of CTAs take 128 of
         // 1408 x 2816 at 400 tokens to 60.8 us from 58.9, at 2048 tokens to 91.5 from 94; parts gain everywhere (400
         // tokens 80 against 96).
-        p.pair = P * p.nt >= (p.mode == kMxA4 ? kMxRows2 : 64);
+        p.pair = p.mode == kMxParts || p.nt >= kMxRows2;
     } else {
-        // Pairs once a token block is wide enough for its operand stream to count: 21504 x 5376 at 64 rows 20.5 us
+        // Parts come from 25 rows on, so in blocks of 64 operand rows at least, and always go to pairs; 4-bit activations
+        // do once a token block is wide enough for its operand stream to count: 21504 x 5376 at 64 rows 20.5 us
         // against 22.3, at 192 rows 27.1 against 30.6.
         p.nt = pair_tokens(P, per, N, K, E, &halved);
-        p.pair = P * p.nt >= 64;
+        p.pair = p.mode == kMxParts || p.nt >= 64;
     }
     p.nblk = (P * p.nt + 127) / 128;
     // Cutting tiles along K costs a zeroed y: worth it while y is small beside the weights.
@@ -446,7 +426,7 @@ cudaError_t launch_mx_gemm(const MxGemm& g, cudaStream_t s) {
     switch (g.plan.mode) {
     case kMxA4: return g.plan.nt <= 64 ? run<kMxA4, 64>(g, s) : run<kMxA4, kMxRows2>(g, s);
     case kMxDigits: return g.plan.nt <= 8 ? run<kMxDigits, 64>(g, s) : run<kMxDigits, kMxRows2>(g, s);
-    default: return run<kMxParts, 64>(g, s);  // wider ones go to pairs
+    default: return cudaErrorInvalidValue;  // parts go to pairs
     }
 }
 

@@ -10,6 +10,14 @@
 // instead of 40.  Each CTA's tensor memory holds the sums of its own weight rows,
 // so the epilogue is the single CTA's.
 //
+// 16-bit activations of many rows come here as two E4M3 parts with scales of their
+// own (kind::mxf8f6f4), x = hi + lo, the low parts being further operand rows:
+// column c of the accumulator is the high part's sum of token c, column n16 + c the
+// low part's, and the epilogue adds them.  The weights' codes are spread to bytes by
+// the copy engine (16 codes to 16 bytes) on their way into shared memory.  A quarter
+// of the digits' tensor work at half its rate, but the spreading copy brings only
+// half as many codes a second, which is what few rows wait for.
+//
 // The even CTA's warp 3 issues all copies of scales to tensor memory and its
 // warp 1 all MMAs, a warp each because a step's six copies and four MMAs take one
 // warp longer to issue (about 32 cycles each, 800 a step with the waits) than the

@@ -56,12 +56,6 @@ __device__ __forceinline__ bool elect() {
 }
 __device__ __forceinline__ int uniform(int v) { return __shfl_sync(kFull, v, 0); }
 
-// Accumulator columns of a block of `rows` tokens.
-template <int MODE>
-__device__ __forceinline__ int columns(int rows) {
-    return MODE == kMxParts ? 2 * mx_pad16(rows) : mx_pad16(mx_planes(MODE) * rows);
-}
-
 struct Tile {
     int expert, row0, rows, wb, slot;
     int k0, k1;  // its steps
