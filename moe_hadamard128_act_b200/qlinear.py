@@ -188,21 +188,14 @@ def _is_mxfp4(fmt: int) -> bool:
     return fmt == MXFP4_G32 or fmt == MXFP4A4_G32
 
 
-def _same_device(what: str, first, *others):
-    device = first.get_device()
-    for t in others:
-        if t is not None and t.get_device() != device:
-            raise ValueError(f"{what}: every tensor must be on the same device")
-
-
 def _mx_check(what: str, fmt: int, N: int, K: int, E: int, x, codes, scales, rows, y, shape, ws):
     """The product's tensors have the sizes and the device that its kernels take for granted."""
     cb, sb, _ = qlinear_packed_sizes(fmt, N, K)
     device = x.get_device()
-    if codes.get_device() != device or scales.get_device() != device or (rows is not None and rows.get_device() != device):
-        _same_device(what, x, codes, scales, rows)
-    if y is not None or ws is not None:
-        _same_device(what, x, y, ws)
+    if (codes.get_device() != device or scales.get_device() != device
+            or (rows is not None and rows.get_device() != device)
+            or (y is not None and y.get_device() != device) or (ws is not None and ws.get_device() != device)):
+        raise ValueError(f"{what}: every tensor must be on the same device")
     if codes.nbytes != E * cb or scales.nbytes != E * sb:
         raise ValueError(f"{what}: {E} x [{N}, {K}] take {E * cb} code and {E * sb} scale bytes")
     if y is not None and (y.dtype != torch.float32 or y.shape != shape):
@@ -255,8 +248,8 @@ def qlinear_pack(fmt: int, N: int, K: int, W: torch.Tensor | None = None, codes:
             raise ValueError(f"W must be an fp32 tensor of shape ({N}, {K})")
         if codes is not None and (codes.nbytes != N * K or scales is None or scales.nbytes != N * K // 32):
             raise ValueError(f"[{N}, {K}] take {N * K} code numbers and {N * K // 32} scales, a byte each")
-        if codes is not None:
-            _same_device("qlinear_pack", codes, scales)
+        if codes is not None and scales.get_device() != codes.get_device():
+            raise ValueError("qlinear_pack: every tensor must be on the same device")
     c_out, s_out = (_new(stream, dev, torch.uint8, max(n, 16)) for n in (cb, sb))
     z_out = _new(stream, dev, torch.uint8, max(zb, 16)) if zb else None
     _on(dev, "qlinear_pack", _ptr(W), _ptr(codes), _ptr(scales), _ptr(zeros), fmt, flags, N, K, _ptr(c_out),
@@ -372,12 +365,15 @@ def mxfp4_dequant(codes: torch.Tensor, scales: torch.Tensor, N: int, K: int, out
     cb, sb, _ = qlinear_packed_sizes(MXFP4_G32, N, K)
     if codes.nbytes != cb or scales.nbytes != sb:
         raise ValueError(f"mxfp4_dequant: [{N}, {K}] takes {cb} code and {sb} scale bytes")
+    device = codes.get_device()
+    if scales.get_device() != device or (out is not None and out.get_device() != device):
+        raise ValueError("mxfp4_dequant: every tensor must be on the same device")
+    device = codes.device
     if out is None:
-        out = _new(stream, codes.device, torch.bfloat16, N, K)
+        out = _new(stream, device, torch.bfloat16, N, K)
     elif out.dtype != torch.bfloat16 or tuple(out.shape) != (N, K):
         raise ValueError(f"out must be a bf16 tensor of shape ({N}, {K})")
-    _same_device("mxfp4_dequant", codes, scales, out)
-    _on(codes.device, "mxfp4_dequant", _ptr(codes), _ptr(scales), N, K, _ptr(out), stream=stream)
+    _on(device, "mxfp4_dequant", _ptr(codes), _ptr(scales), N, K, _ptr(out), stream=stream)
     return out
 
 
