@@ -133,8 +133,10 @@ def _ptr(t: torch.Tensor | None):
     return t.data_ptr()
 
 
-_device = torch._C._cuda_getDevice
-_raw_stream = torch._C._cuda_getCurrentRawStream
+# The reads that torch.cuda.current_device and current_stream make, without their objects; a torch without CUDA has
+# neither, and then no call but those of sizes.
+_device = getattr(torch._C, "_cuda_getDevice", torch.cuda.current_device)
+_raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None)
 
 
 def _stream(stream=None):

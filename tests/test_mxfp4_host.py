@@ -2,6 +2,8 @@
 before anything is launched."""
 import ctypes
 import re
+import subprocess
+import sys
 from pathlib import Path
 
 import numpy as np
@@ -252,3 +254,17 @@ def test_binding_refuses_tensors_of_two_devices(Q, monkeypatch):
                 with pytest.raises(ValueError, match="the same device"):
                     call()
                 places[id(t)] = 0
+
+
+def test_binding_imports_beside_a_torch_without_cuda(Q):
+    # such a torch lacks the CUDA parts of torch._C: names, constants and sizes are there all the same
+    code = """
+import torch
+for name in ("_cuda_getDevice", "_cuda_getCurrentRawStream"):
+    if hasattr(torch._C, name):
+        delattr(torch._C, name)
+from moe_hadamard128_act_b200 import qlinear as Q
+assert Q.qlinear_packed_sizes(Q.MXFP4_G32, 128, 256) == (128 * 128, 1024, 0)
+assert Q.qlinear_workspace_size(Q.MXFP4A4_G32, 0, 1, 128, 256) > 0
+"""
+    subprocess.run([sys.executable, "-c", code], cwd=ROOT, check=True, timeout=300)
