@@ -161,12 +161,17 @@ def _empty(nbytes: int, device) -> torch.Tensor:
     return torch.empty(max(int(nbytes), 16), dtype=torch.uint8, device=device)
 
 
-def _new(stream, device, dtype, *size) -> torch.Tensor:
-    """A tensor of the stream that the call runs on, so that its memory is not handed on while the call runs."""
+def _new(stream, device, dtype, *size, scratch: bool = False) -> torch.Tensor:
+    """A tensor of the stream that the call runs on, so that its memory is not handed on while the call runs; nor, if it
+    is a result, while the caller's current stream still has work that was queued with it."""
     if stream is None:
         return torch.empty(*size, dtype=dtype, device=device)  # sizes as arguments: faster than a tuple
+    current = torch.cuda.current_stream(device)
     with torch.cuda.stream(stream):
-        return torch.empty(*size, dtype=dtype, device=device)
+        t = torch.empty(*size, dtype=dtype, device=device)
+    if not scratch and current != stream:
+        t.record_stream(current)
+    return t
 
 
 def _output(y, stream, device, *size):
@@ -182,7 +187,7 @@ def _workspace(ws, need: int, stream, device):
     if ws is not None and ws.nbytes >= need:
         return ws, _ptr(ws), ws.nbytes
     need = max(need, 16)
-    ws = _new(stream, device, torch.uint8, need)
+    ws = _new(stream, device, torch.uint8, need, scratch=True)
     return ws, ws.data_ptr(), need
 
 

@@ -167,3 +167,28 @@ def test_pairs_that_gave_up_leave_nothing_behind(Q, fmt, limit):
         assert status in ((6, Q.DEVERR_TIMEOUT), (0, 0)) and (limit > 1 or status[0] == 6)
         close(y[0], *ref)
         close(y[1], *few)
+
+
+# ---- streams ------------------------------------------------------------------------------------------------
+@pytest.mark.parametrize("fmt", FMTS)
+def test_results_of_a_side_stream_outlive_what_the_current_stream_does_with_them(Q, fmt):
+    # the current stream reads a result late; later calls on the side stream, which wait for nothing, take other memory
+    N, K, M = 300, 512, 40
+    c, s, W = weight(Q, N, K)
+    inputs = [x_bits(M, K, seed=20 + i) for i in range(4)]
+    xs = [dev_bf16(x) for x in inputs]
+    side, main = torch.cuda.Stream(), torch.cuda.current_stream()
+    torch.cuda.synchronize()
+    read = []
+    for xd in xs:
+        y = Q.qlinear_forward(xd, c, s, None, fmt, N, stream=side)
+        codes, scales = Q.act_quant_mxfp4(xd, stream=side)
+        main.wait_stream(side)
+        torch.cuda._sleep(5_000_000)
+        read.append((y.clone(), codes.clone(), scales.clone()))
+        del y, codes, scales
+    torch.cuda.synchronize()
+    for x, xd, (y, codes, scales) in zip(inputs, xs, read):
+        close(y, *X.forward(x, W, fmt))
+        again = Q.act_quant_mxfp4(xd)
+        assert torch.equal(codes, again[0]) and torch.equal(scales, again[1])
