@@ -343,7 +343,7 @@ constexpr int kPairs = kPlanSms / 2;
 // along K: the cut with the least rounds of tiles times what a tile of so many operand rows takes.  Measured at 5376
 // columns, 74 x 256 weight rows and 2048 rows of 4-bit x, a round of 64, 96, 128, 160, 192, 208 and 256 operand rows
 // takes 5.4, 6.1, 6.1, 7.0, 8.4, 8.8 and 9.9 us, one of 16-bit parts half as much again, but no less than the spreading
-// copies' 9.4.
+// copies' 9.4.  Other widths are taken to go with K, which leaves out a tile's start and epilogue at small K.
 // Halves, of one weight's tiles that leave half of the pairs without work, cost zeroed outputs and adding into them, 2 us
 // and half a us for every MB: 5376 x 21504 at 128 rows takes 22.9 us with them and 29.3 without (4-bit x) and 38.9
 // against 49.4 (parts), but 4096 x 4096 at 256 rows 15.3 against 12.8.  After full rounds only parts gain (21504 x 5376
